@@ -48,6 +48,7 @@ extern "C" {
 
 #define DUOLM_DTYPE_FP32 0     /* fp32 weights, fp32 arithmetic everywhere */
 #define DUOLM_DTYPE_BF16 1     /* bf16 weights; fp16 tensor-core operands, fp32 accumulate */
+#define DUOLM_DTYPE_FP16 2     /* fp16 elements (paged caches only; not a model dtype) */
 
 #define DUOLM_MODE_MIS 0          /* shared prefix + tree-masked branches */
 #define DUOLM_MODE_INDEPENDENT 1  /* every candidate as its own full sequence */
@@ -236,7 +237,7 @@ int64_t duolm_launches_per_execute(const duolm_ctx *ctx);
 
 /* Text of the last failure on this context ("" if none).  Valid until the
  * next call on the context.  With ctx == NULL: the reason the calling
- * thread's last context-free call (duolm_model_load, duolm_compile) failed. */
+ * thread's last context-free call (duolm_model_load, duolm_compile, duolm_pages_*) failed. */
 const char *duolm_last_error(const duolm_ctx *ctx);
 
 /* Free every device resource of the context (NULL is ignored). */
@@ -373,6 +374,163 @@ int duolm_gather(duolm_ctx *ctx, const int32_t *ids, int64_t n, float *x, uint16
  */
 int duolm_embedding_rho_static(const void *embed, int dtype, int64_t vocab, int d, double *rho_out,
                                void *cuda_stream);
+
+/* ---- paged KV cache ------------------------------------------------------
+ *
+ * The prefix KV store above keeps each session in one fixed slot.  A paged
+ * cache keeps sequences of any length in pages of page_tokens tokens taken
+ * from one pool, lets sequences that begin alike share pages, and is read by
+ * a chunk attention through its page table.  It belongs to no context: every
+ * array is the caller's device memory, every call only enqueues work on
+ * cuda_stream (NULL: the default stream) of the cache's device, allocates
+ * nothing, reads lengths and tables on the device, and can be captured into
+ * a graph and replayed as the lengths go on.
+ *
+ * Errors that the host can see are returned at once (the reason in
+ * duolm_last_error(NULL)).  What only the device can see (too few free pages,
+ * a sequence id or length out of range) raises the cache's status word: a
+ * call of duolm_pages_resize, _fork or _plan that raises it changes nothing
+ * else, and every later call on the cache does nothing until
+ * duolm_pages_check reports and clears it.  A page id out of range in the
+ * caller's tables is never followed.
+ *
+ * Calls that use the same cache, workspace or plan must be ordered on the
+ * GPU (one stream, or events between streams); two calls that overlap race.
+ * That holds for two captured graphs with one plan, too.
+ */
+typedef struct {
+  int32_t device;
+  int32_t dtype;         /* DUOLM_DTYPE_FP32, _BF16 or _FP16: elements of k and v */
+  int32_t n_layers;
+  int32_t n_kv_heads;
+  int32_t head_dim;      /* 64 or 128; fp32: a multiple of 32 up to 256 */
+  int32_t page_tokens;   /* a power of two, 8 to 256 */
+  int32_t n_pages;       /* n_pages * n_kv_heads * page_tokens < 2^31 */
+  int32_t n_seqs;        /* at most 2^20 */
+  int32_t max_pages;     /* pages of the longest sequence; max_pages * page_tokens < 2^30 */
+  int32_t reserved;      /* 0 */
+  void *k, *v;           /* [n_layers][n_pages][n_kv_heads][page_tokens][head_dim], 16-byte aligned */
+  int32_t *table;        /* [n_seqs][max_pages]: token t of a sequence is slot t % page_tokens of page
+                          * table[seq][t / page_tokens]; entries behind its length are not read */
+  int32_t *length;       /* [n_seqs] tokens; an unused sequence has 0 */
+  int32_t *refs;         /* [n_pages] sequences that hold the page; 0: free */
+  void *status;          /* 16 bytes, 16-byte aligned, zeroed once by the caller */
+  void *workspace;       /* duolm_pages_workspace() bytes, 16-byte aligned, any contents */
+  int64_t workspace_bytes;
+} duolm_pages;
+
+/* Bytes of duolm_pages.workspace, or a negative code. */
+int64_t duolm_pages_workspace(int64_t n_pages, int64_t n_seqs);
+
+/*
+ * duolm_pages_resize: entry i's sequence seq[i] gets length[i] tokens
+ * (device int32 [n]; length NULL: all 0, which frees the sequences).
+ *   Growing takes the lowest free pages, in entry order.  Where a sequence
+ *   grows out of a partly filled page that other sequences hold too, it first
+ *   gets a copy of that page's filled rows, in every layer (copy on write);
+ *   the copy is the entry's first new page.  New rows hold whatever the page
+ *   held before.
+ *   Shrinking gives back the pages behind the new length.
+ * Pages given back by this call are free for later calls, not for this one.
+ * A sequence may appear once.  Returns DUOLM_E_ARG for n < 0, n > n_seqs or
+ * a null array.  Raises: a bad or repeated sequence, a length below 0 or
+ * above max_pages * page_tokens, too few free pages.
+ */
+int duolm_pages_resize(const duolm_pages *pages, int n, const int32_t *seq, const int32_t *length, void *cuda_stream);
+
+/*
+ * duolm_pages_fork: sequence dst[i] (length 0 until now) begins as the first
+ * tokens[i] tokens of src[i], sharing their pages (device int32 [n] each; no
+ * K or V is copied until one of them grows, see duolm_pages_resize).  A
+ * source may appear several times, a destination once and not as a source
+ * of the same call.  Raises: a bad or repeated sequence, a destination that
+ * is not empty, tokens outside 0..length.
+ */
+int duolm_pages_fork(const duolm_pages *pages, int n, const int32_t *src, const int32_t *dst, const int32_t *tokens,
+                     void *cuda_stream);
+
+/*
+ * duolm_pages_compact: move the live pages to ids 0 .. n_live - 1.  The k-th
+ * live page at n_live or above goes to the k-th free page below n_live; no
+ * other page is written.  table_out [n_seqs][max_pages] (-1 behind each
+ * length) and refs_out [n_pages] receive the tables that go with the new
+ * places and live_out[0] the count; they may be the cache's own table and
+ * refs.  With other arrays the old tables stay valid for readers until
+ * pages are next taken, since the old copies are left as they were.
+ */
+int duolm_pages_compact(const duolm_pages *pages, int32_t *table_out, int32_t *refs_out, int32_t *live_out,
+                        void *cuda_stream);
+
+/* Wait for cuda_stream, report what the device raised since the last check
+ * and clear it: DUOLM_E_CAPACITY (too few free pages), DUOLM_E_ARG (a
+ * sequence, length, offset or position out of range), DUOLM_E_DEVICE (a page
+ * id out of range, a wait that ran out).  Not inside a capture. */
+int duolm_pages_check(const duolm_pages *pages, void *cuda_stream);
+
+/*
+ * A batch of query rows: entry i is the rows offset[i] .. offset[i + 1] - 1
+ * of the callers' arrays and belongs to sequence seq[i].  In a causal batch
+ * (and for duolm_pages_write) they are the sequence's last tokens: with R rows
+ * and length L, row j is token L - R + j.
+ */
+typedef struct {
+  int32_t n;              /* entries */
+  int32_t n_rows;         /* rows of the arrays; offset[n] may be less: rows behind it are left alone */
+  int32_t max_rows;       /* no entry has more rows (chooses the kernel; a larger entry is still right) */
+  int32_t n_q_heads;      /* a multiple of n_kv_heads, at most 64 times as many */
+  int32_t causal;         /* 1: row j sees the tokens up to its own; 0: every row sees the whole sequence */
+  int32_t reserved;       /* 0 */
+  const int32_t *seq;     /* device [n], each sequence once */
+  const int32_t *offset;  /* device [n + 1], from 0, not decreasing */
+  void *plan;             /* duolm_pages_plan_bytes() bytes, 128-byte aligned */
+  int64_t plan_bytes;
+} duolm_pages_batch;
+
+/* Bytes of a batch's plan, or a negative code. */
+int64_t duolm_pages_plan_bytes(const duolm_pages *pages, int n, int n_rows, int max_rows, int n_q_heads);
+
+/*
+ * duolm_pages_plan: from the batch and the cache's lengths and tables as they
+ * are now (after duolm_pages_resize), where each row's token lies and how the
+ * attention's key tiles are divided among the SMs.  Once per step, for the
+ * calls below on every layer.  Raises: a bad or repeated sequence, an offset
+ * or length out of range.
+ */
+int duolm_pages_plan(const duolm_pages *pages, const duolm_pages_batch *batch, void *cuda_stream);
+
+/*
+ * duolm_pages_write: a layer's projections into the cache.  Every q and k head
+ * is RMS-normalised over head_dim (gains q_gain, k_gain: device float
+ * [head_dim], NULL: no norm) and its pairs (i, i + head_dim / 2) are rotated
+ * by rope[position][i] = (cos, sin) (device float [rope_positions][head_dim /
+ * 2][2], 16-byte aligned, NULL: no rotation), in fp32, rounded once.  k goes
+ * to its token's slot, v there unchanged, q to q_out (which may be q).
+ *   q, q_out: [n_rows][n_q_heads][head_dim], NULL q: K and V only;
+ *   k, v: [n_rows][n_kv_heads][head_dim]; elements of the cache's dtype.
+ * Strides are elements from row to row; rows must be 16-byte aligned.
+ * Raises: an entry with more rows than its sequence has tokens, a position
+ * not in rope.
+ */
+int duolm_pages_write(const duolm_pages *pages, const duolm_pages_batch *batch, int layer, const void *q,
+                      int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                      const float *q_gain, const float *k_gain, float eps, const float *rope, int64_t rope_positions,
+                      void *q_out, int64_t q_out_stride, void *cuda_stream);
+
+/*
+ * duolm_pages_attention: out[row][h] = sum over the tokens t the row sees of
+ * softmax_t(scale * q[row][h] . k_t) v_t, with KV head h / (n_q_heads /
+ * n_kv_heads).  q and out: [n_rows][n_q_heads][head_dim] of the cache's dtype,
+ * rows 16-byte aligned, strides in elements; lse (NULL or float
+ * [n_rows][n_q_heads]): the natural log of the softmax's sum, with which
+ * results over different tokens can be joined.  A row that sees no token
+ * gives zeros and -infinity.  scale > 0.  Slots behind a sequence's length
+ * may hold anything; K and V of its own tokens must be finite.  Scores,
+ * maxima, sums and out are accumulated in fp32; with 16-bit elements the
+ * softmax's weights are rounded to them before they meet V.  The result does
+ * not depend on the order in which CTAs finish.
+ */
+int duolm_pages_attention(const duolm_pages *pages, const duolm_pages_batch *batch, int layer, const void *q,
+                          int64_t q_stride, float scale, void *out, int64_t out_stride, float *lse, void *cuda_stream);
 
 /* ---- introspection (tests) --------------------------------------------- */
 

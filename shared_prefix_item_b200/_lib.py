@@ -17,6 +17,7 @@ lib_path = os.path.join(_HERE, "libduolm.so")
 
 DTYPE_FP32 = 0
 DTYPE_BF16 = 1
+DTYPE_FP16 = 2  # paged caches
 MODE_MIS = 0
 MODE_INDEPENDENT = 1
 
@@ -42,6 +43,18 @@ class Template(ctypes.Structure):
                 ("instr", ctypes.c_void_p), ("n_instr", ctypes.c_int32),
                 ("header", ctypes.c_void_p), ("n_header", ctypes.c_int32),
                 ("branch_header", ctypes.c_void_p), ("n_branch_header", ctypes.c_int32)]
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("device", "dtype", "n_layers", "n_kv_heads", "head_dim", "page_tokens",
+                                              "n_pages", "n_seqs", "max_pages", "reserved")] + \
+               [(f, ctypes.c_void_p) for f in ("k", "v", "table", "length", "refs", "status", "workspace")] + \
+               [("workspace_bytes", ctypes.c_int64)]
+
+
+class PagesBatch(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("n", "n_rows", "max_rows", "n_q_heads", "causal", "reserved")] + \
+               [(f, ctypes.c_void_p) for f in ("seq", "offset", "plan")] + [("plan_bytes", ctypes.c_int64)]
 
 
 def _load():
@@ -84,6 +97,15 @@ def _load():
         "duolm_kv_slot_length": (I, [VP, I]),
         "duolm_prepare_cached": (I, [VP, I, VP, VP, VP, VP, I, VP, VP, VP]),
         "duolm_score_cached": (I, [VP, I, VP, VP, VP, VP, I, VP, VP, VP, VP]),
+        "duolm_pages_workspace": (I64, [I64, I64]),
+        "duolm_pages_resize": (I, [VP, I, VP, VP, VP]),
+        "duolm_pages_fork": (I, [VP, I, VP, VP, VP, VP]),
+        "duolm_pages_compact": (I, [VP, VP, VP, VP, VP]),
+        "duolm_pages_check": (I, [VP, VP]),
+        "duolm_pages_plan_bytes": (I64, [VP, I, I, I, I]),
+        "duolm_pages_plan": (I, [VP, VP, VP]),
+        "duolm_pages_write": (I, [VP, VP, I, VP, I64, VP, I64, VP, I64, VP, VP, ctypes.c_float, VP, I64, VP, I64, VP]),
+        "duolm_pages_attention": (I, [VP, VP, I, VP, I64, ctypes.c_float, VP, I64, VP, VP]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -358,3 +380,180 @@ class Ranker:
         out = np.empty((n_items, self.d), np.uint16)
         self._check(lib.duolm_debug_table(self.ctx, _p(out), int(n_items)))
         return out
+
+
+# ---- paged KV cache ----------------------------------------------------------
+# Device arrays are tensors that know their data_ptr(), shape, stride(), dtype
+# and device (torch tensors); they are checked and passed as pointers, never
+# copied.  ``stream`` is a cudaStream_t handle (None: the default stream).
+
+_PAGE_DTYPES = {"torch.float32": DTYPE_FP32, "torch.bfloat16": DTYPE_BF16, "torch.float16": DTYPE_FP16}
+
+
+def _on(t, name: str, device: int):
+    d = t.device
+    if d.type != "cuda" or d.index != device:
+        raise ValueError(f"{name} is on {d}, the cache on cuda:{device}")
+    return t
+
+
+def _ints(t, name: str, device: int, shape=None) -> int:
+    """Pointer of a contiguous int32 device array of this shape (None: any 1-D)."""
+    _on(t, name, device)
+    if str(t.dtype) != "torch.int32" or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 array is wanted")
+    if (t.dim() != 1) if shape is None else (tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {'one dimension' if shape is None else tuple(shape)} wanted")
+    return t.data_ptr()
+
+
+def _bytes(t, name: str, device: int) -> int:
+    _on(t, name, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous array is wanted")
+    return t.numel() * t.element_size()
+
+
+class PagedCache:
+    """A paged KV cache over the caller's device arrays: k and v
+    [n_layers, n_pages, n_kv_heads, page_tokens, head_dim] (fp32, bf16 or
+    fp16), int32 table [n_seqs, max_pages], length [n_seqs] and refs
+    [n_pages], a zeroed status of 16 bytes and a workspace of
+    ``workspace_bytes(n_pages, n_seqs)`` bytes.  The methods call the C entry
+    points of the same names (``duolm_pages_<name>``)."""
+
+    def __init__(self, k, v, table, length, refs, status, workspace):
+        if k.dim() != 5 or tuple(v.shape) != tuple(k.shape) or v.dtype != k.dtype:
+            raise ValueError("k and v: [n_layers, n_pages, n_kv_heads, page_tokens, head_dim], alike")
+        if str(k.dtype) not in _PAGE_DTYPES:
+            raise ValueError(f"k and v of {k.dtype}: fp32, bf16 or fp16 is wanted")
+        if table.dim() != 2:
+            raise ValueError("table: [n_seqs, max_pages]")
+        if k.device.type != "cuda":
+            raise ValueError(f"k is on {k.device}: a paged cache lives on a GPU")
+        L, N, H, P, D = k.shape
+        S, M = table.shape
+        dev = k.device.index
+        _bytes(k, "k", dev), _bytes(v, "v", dev)
+        if _bytes(status, "status", dev) < 16:
+            raise ValueError("status: 16 bytes are wanted")
+        self.desc = Pages(dev, _PAGE_DTYPES[str(k.dtype)], L, H, D, P, N, S, M, 0, k.data_ptr(), v.data_ptr(),
+                          _ints(table, "table", dev, (S, M)), _ints(length, "length", dev, (S,)),
+                          _ints(refs, "refs", dev, (N,)), status.data_ptr(), workspace.data_ptr(),
+                          _bytes(workspace, "workspace", dev))
+        self._arrays = (k, v, table, length, refs, status, workspace)  # kept alive with their pointers
+        self._ref = ctypes.byref(self.desc)
+        self.device, self.dtype = dev, k.dtype
+        self.n_kv_heads, self.head_dim = H, D
+
+    @staticmethod
+    def workspace_bytes(n_pages: int, n_seqs: int) -> int:
+        return _pages_rc(lib.duolm_pages_workspace(int(n_pages), int(n_seqs)))
+
+    def resize(self, seq, length, stream: Optional[int] = None):
+        """Sequence seq[i] gets length[i] tokens (None: all 0)."""
+        n = seq.shape[0]
+        _pages_rc(lib.duolm_pages_resize(self._ref, n, _ints(seq, "seq", self.device),
+                                         None if length is None else _ints(length, "length", self.device, (n,)), stream))
+
+    def free(self, seq, stream: Optional[int] = None):
+        """The sequences' pages are given back."""
+        self.resize(seq, None, stream)
+
+    def fork(self, src, dst, tokens, stream: Optional[int] = None):
+        """The empty sequence dst[i] begins as the first tokens[i] tokens of src[i]."""
+        n = src.shape[0]
+        _pages_rc(lib.duolm_pages_fork(self._ref, n, _ints(src, "src", self.device), _ints(dst, "dst", self.device, (n,)),
+                                       _ints(tokens, "tokens", self.device, (n,)), stream))
+
+    def compact(self, table_out, refs_out, live_out, stream: Optional[int] = None):
+        """Live pages move to the lowest ids; the tables that go with them are
+        written to the outputs (which may be the cache's own)."""
+        d = self.desc
+        _pages_rc(lib.duolm_pages_compact(self._ref, _ints(table_out, "table_out", self.device, (d.n_seqs, d.max_pages)),
+                                          _ints(refs_out, "refs_out", self.device, (d.n_pages,)),
+                                          _ints(live_out, "live_out", self.device, (1,)), stream))
+
+    def check(self, stream: Optional[int] = None):
+        """Waits for the stream; DuolmError for what the device raised since
+        the last check, which is cleared."""
+        _pages_rc(lib.duolm_pages_check(self._ref, stream))
+
+    def plan_bytes(self, n: int, n_rows: int, max_rows: int, n_q_heads: int) -> int:
+        return _pages_rc(lib.duolm_pages_plan_bytes(self._ref, int(n), int(n_rows), int(max_rows), int(n_q_heads)))
+
+    def batch(self, seq, offset, n_rows: int, max_rows: int, n_q_heads: int, plan, causal: bool = True) -> "PagedBatch":
+        """A batch of query rows over this cache: entry i is rows offset[i] ..
+        offset[i + 1] - 1 and belongs to sequence seq[i]; plan is a buffer of
+        ``plan_bytes`` bytes."""
+        return PagedBatch(self, seq, offset, n_rows, max_rows, n_q_heads, plan, causal)
+
+
+class PagedBatch:
+    """See ``PagedCache.batch``.  ``plan`` once per step, then ``write`` and
+    ``attention`` for every layer."""
+
+    def __init__(self, cache: PagedCache, seq, offset, n_rows, max_rows, n_q_heads, plan, causal):
+        n, dev = seq.shape[0], cache.device
+        self.desc = PagesBatch(n, int(n_rows), int(max_rows), int(n_q_heads), 1 if causal else 0, 0,
+                               _ints(seq, "seq", dev), _ints(offset, "offset", dev, (n + 1,)), plan.data_ptr(),
+                               _bytes(plan, "plan", dev))
+        self.cache = cache
+        self._arrays = (seq, offset, plan)
+        self._ref = ctypes.byref(self.desc)
+
+    def _rows(self, t, name: str, heads: int):
+        """(pointer, row stride) of [n_rows, heads, head_dim] rows, or [n_rows, heads * head_dim]."""
+        c = self.cache
+        _on(t, name, c.device)
+        if t.dtype != c.dtype:
+            raise ValueError(f"{name} of {t.dtype}, the cache of {c.dtype}")
+        want, st = (self.desc.n_rows, heads, c.head_dim), t.stride()
+        flat = t.dim() == 2 and tuple(t.shape) == (want[0], heads * c.head_dim) and st[1] == 1
+        if not flat and not (tuple(t.shape) == want and st[2] == 1 and (heads == 1 or st[1] == c.head_dim)):
+            raise ValueError(f"{name}: shape {tuple(t.shape)} strides {st}, rows of {heads} x {c.head_dim} contiguous "
+                             f"elements ({want[0]} of them) are wanted")
+        return t.data_ptr(), (st[0] if want[0] > 1 else heads * c.head_dim)
+
+    def _floats(self, t, name: str, shape) -> Optional[int]:
+        if t is None:
+            return None
+        _on(t, name, self.cache.device)
+        if str(t.dtype) != "torch.float32" or not t.is_contiguous() or (shape and tuple(t.shape) != shape):
+            raise ValueError(f"{name}: contiguous float32 {shape or ''} is wanted, got {t.dtype} {tuple(t.shape)}")
+        return t.data_ptr()
+
+    def plan(self, stream: Optional[int] = None):
+        _pages_rc(lib.duolm_pages_plan(self.cache._ref, self._ref, stream))
+
+    def write(self, layer: int, q, k, v, q_out, q_gain=None, k_gain=None, eps: float = 1e-6, rope=None,
+              stream: Optional[int] = None):
+        """K and V of the batch's rows into the cache, q (None: none) to
+        q_out, with QK-norm (gains [head_dim]) and rotation (rope
+        [positions, head_dim / 2, 2])."""
+        c, hd = self.cache, self.cache.head_dim
+        kp, ks = self._rows(k, "k", c.n_kv_heads)
+        vp, vs = self._rows(v, "v", c.n_kv_heads)
+        qp, qs = self._rows(q, "q", self.desc.n_q_heads) if q is not None else (None, 0)
+        op, os_ = self._rows(q_out, "q_out", self.desc.n_q_heads) if q is not None else (None, 0)
+        if rope is not None and (rope.dim() != 3 or tuple(rope.shape[1:]) != (hd // 2, 2)):
+            raise ValueError(f"rope: [positions, {hd // 2}, 2] is wanted, got {tuple(rope.shape)}")
+        _pages_rc(lib.duolm_pages_write(c._ref, self._ref, int(layer), qp, qs, kp, ks, vp, vs,
+                                        self._floats(q_gain, "q_gain", (hd,)), self._floats(k_gain, "k_gain", (hd,)),
+                                        float(eps), self._floats(rope, "rope", None), 0 if rope is None else rope.shape[0],
+                                        op, os_, stream))
+
+    def attention(self, layer: int, q, out, lse, scale: float, stream: Optional[int] = None):
+        """Attention of the batch's rows over their sequences' pages; lse
+        (None, or float32 [n_rows, n_q_heads]) the log of the softmax's sum."""
+        c, h = self.cache, self.desc.n_q_heads
+        qp, qs = self._rows(q, "q", h)
+        op, os_ = self._rows(out, "out", h)
+        _pages_rc(lib.duolm_pages_attention(c._ref, self._ref, int(layer), qp, qs, float(scale), op, os_,
+                                            self._floats(lse, "lse", (self.desc.n_rows, h)), stream))
+
+
+def _pages_rc(rc: int) -> int:
+    if rc < 0:
+        raise DuolmError(rc, lib.duolm_last_error(None).decode())
+    return rc

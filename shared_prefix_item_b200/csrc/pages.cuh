@@ -1,0 +1,221 @@
+// Paged KV cache: what its kernels share (host and device).
+//
+// A cache is K and V [n_layers][n_pages][n_kv_heads][page_tokens][head_dim];
+// token t of a sequence is slot t % page_tokens of page table[seq][t /
+// page_tokens].  Every array belongs to the caller and lives on the device,
+// so every call is stream-ordered work that a graph can capture: lengths and
+// tables are read on the device, never on the host.
+//
+// Every kernel reads the cache's status word first and does nothing while it
+// is raised, so a call that was refused on the device (no free pages, a bad
+// sequence) is not followed by writes that count on it; duolm_pages_check
+// reports and clears it.
+#pragma once
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "duolm.h"
+
+namespace duolm {
+
+enum : uint32_t {  // further bits of the cache's status word
+  ERR_NO_PAGES = 8u,     // fewer free pages than the call needs
+  ERR_BAD_SEQ = 16u,     // a sequence id out of range, twice in a call, or in the wrong state
+  ERR_BAD_LENGTH = 32u,  // a length, token count or offset out of range
+};
+
+struct PagesView {
+  char* k;
+  char* v;
+  int32_t* table;
+  int32_t* length;
+  int32_t* refs;
+  DevStatus* st;
+  int n_layers, n_kv_heads, head_dim, page_tokens, page_shift, n_pages, n_seqs, max_pages, elem;
+
+  __host__ __device__ int64_t head_bytes() const { return (int64_t)page_tokens * head_dim * elem; }
+  __host__ __device__ int64_t page_bytes() const { return n_kv_heads * head_bytes(); }
+  __host__ __device__ int64_t layer_bytes() const { return n_pages * page_bytes(); }
+  __host__ __device__ int pages_of(int tokens) const { return (tokens + page_tokens - 1) >> page_shift; }
+  __host__ __device__ int max_tokens() const { return max_pages << page_shift; }
+};
+
+// Read once per kernel, after pdl_wait().
+__device__ __forceinline__ bool pages_raised(const PagesView& p) {
+  return *reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0;
+}
+
+// ---- one CTA deciding for a whole call ----------------------------------------
+constexpr int kPlanThreads = 1024;
+
+// Exclusive prefix sum over the block's kPlanThreads values of 0..kScanCap;
+// *total: their sum, where that is below kScanCap, else kScanCap (callers
+// refuse it).  Uses s[32]; ends with the block in step.
+constexpr int kScanCap = 1 << 29;
+__device__ __forceinline__ int block_scan(int v, int* s, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = min(x + y, kScanCap);
+  }
+  if (lane == 31) s[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = s[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y = min(y + z, kScanCap);
+    }
+    s[lane] = y;
+  }
+  __syncthreads();
+  const int before = warp ? s[warp - 1] : 0;
+  *total = s[31];
+  __syncthreads();
+  return before + x - v;
+}
+
+// true for the first call with this id in the block
+__device__ __forceinline__ bool claim(uint32_t* seen, int id) {
+  return !(atomicOr(&seen[id >> 5], 1u << (id & 31)) >> (id & 31) & 1u);
+}
+
+// ---- bookkeeping workspace ---------------------------------------------------
+// int32 words: [0] page copies, [1] live pages; then the arrays below.
+struct PageCopy {
+  int src, dst, rows, refs;
+};
+struct PagesWork {
+  int32_t* head;     // [16]
+  PageCopy* copies;  // [max(n_seqs, n_pages)]
+  int32_t* list;     // [n_pages] free pages, or compact's holes
+  int32_t* map;      // [n_pages] compact: new id of each live page, -1 otherwise
+  int4* entry;       // [n_seqs] resize: {first of its pages in `list`, pages before, pages after, copy on write}
+};
+inline int64_t pages_work_bytes(int64_t n_pages, int64_t n_seqs) {
+  return 64 + 16 * std::max(n_pages, n_seqs) + 16 * n_seqs + 8 * n_pages;
+}
+inline PagesWork pages_work(void* ws, int64_t n_pages, int64_t n_seqs) {
+  char* b = static_cast<char*>(ws);
+  PagesWork w;
+  w.head = reinterpret_cast<int32_t*>(b);
+  w.copies = reinterpret_cast<PageCopy*>(b + 64);
+  b += 64 + 16 * std::max(n_pages, n_seqs);
+  w.entry = reinterpret_cast<int4*>(b);
+  b += 16 * n_seqs;
+  w.list = reinterpret_cast<int32_t*>(b);
+  w.map = w.list + n_pages;
+  return w;
+}
+
+// ---- batch plan --------------------------------------------------------------
+// Which kernel reads the batch, decided by the host from sizes alone.
+enum PagesPath { kPathSimt16 = 0, kPathSimt64 = 1 };
+struct PathShape {
+  int slots;     // (token, query head) rows of one item
+  int keys;      // keys of one tile
+  int part_words;  // fp32 words of one partial result: slots x (head_dim + 2)
+};
+PagesPath pages_path(int dtype, int64_t max_rows, int group);
+PathShape pages_path_shape(PagesPath path, int head_dim);
+
+// One piece of attention work: the query rows [row0, row0 + n_rows) of one
+// entry under one KV head.  Row j sees keys [0, min(last0 + j + 1, n_keys))
+// when causal, [0, n_keys) otherwise.
+struct PageItem {
+  int seq, kv_head, row0, n_rows;
+  int last0, n_keys, unit0, n_tiles;  // unit0: key tiles of all items before it
+};
+static_assert(sizeof(PageItem) == 32, "item layout");
+
+constexpr int kRowNone = -1;     // a row behind the last entry's
+constexpr int kRowOutside = -2;  // more rows than the sequence has tokens: nowhere to write
+
+struct PlanHead {
+  int n_items;
+  int units;  // key tiles of all items; CTA c of n takes [c units / n, (c + 1) units / n)
+  int ctas;   // CTAs that take part: all, or one per unit where there are fewer
+  int pad[13];
+};
+struct PagesPlan {
+  PlanHead* head;
+  int32_t* cta_item;  // [ctas] item holding the CTA's first unit
+  int32_t* arrived;   // [max_items] finished parts of a divided item (0 between calls)
+  PageItem* items;    // [max_items]
+  int2* base;         // [n + 1] per entry: items and units before it
+  int2* rows;         // [n_rows] {page * page_tokens + slot, position}; x: kRowNone, kRowOutside
+  float* parts;       // [2 ctas][part_words]
+  int max_items, ctas;
+};
+// Layout of a plan for n entries and n_rows query rows; returns its bytes.
+int64_t pages_plan_layout(char* base, int64_t n, int64_t n_rows, int n_kv_heads, int group, PathShape sh, int ctas,
+                          PagesPlan* out);
+
+// first unit of CTA c
+__host__ __device__ inline int cta_unit(int64_t c, int64_t units, int ctas) { return (int)(c * units / ctas); }
+// CTA that runs unit u
+__host__ __device__ inline int unit_cta(int64_t u, int64_t units, int ctas) {
+  return (int)(((u + 1) * ctas + units - 1) / units) - 1;
+}
+
+// ---- the attention's parts joined --------------------------------------------
+// An item whose key tiles are divided among CTAs c0..c1 is finished by
+// whichever of them arrives last: every CTA stores its part (unnormalised O
+// and the row statistics), the last one reads all parts in CTA order, so the
+// result does not depend on the order of arrival.  A CTA holds at most two
+// parts: slot 2c for an item begun before it, 2c + 1 for one begun by it.
+struct CtaWork {  // a CTA's units [unit, end), the first of them in item `item`
+  int unit, end, item, units, ctas;
+};
+__device__ __forceinline__ CtaWork cta_work(const PagesPlan& pl, int cta) {
+  CtaWork w{0, 0, 0, pl.head->units, pl.head->ctas};
+  if (pl.head->n_items == 0 || cta >= w.ctas) return w;
+  w.unit = cta_unit(cta, w.units, w.ctas);
+  w.end = cta_unit(cta + 1, w.units, w.ctas);
+  w.item = pl.cta_item[cta];
+  return w;
+}
+__device__ __forceinline__ float* part_of(const PagesPlan& pl, int part_words, int cta, bool begun_here) {
+  return pl.parts + (int64_t)(2 * cta + (begun_here ? 1 : 0)) * part_words;
+}
+
+// kernels (pages_attention.cu)
+struct AttnArgs {
+  const char* q;
+  char* o;
+  float* lse;
+  int64_t q_stride, o_stride;  // elements between rows
+  int n_q_heads, group, causal, layer;
+  float scale;
+};
+cudaError_t pages_attention_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, int dtype, bool few,
+                                 cudaStream_t s);
+
+// host helpers (pages.cu)
+int pages_fail(int code, const char* fmt, ...);
+int pages_view(const duolm_pages* p, PagesView* out);
+int pages_sms(int device);
+
+// makes a device current for one call
+class DeviceGuard {
+ public:
+  explicit DeviceGuard(int device) {
+    if (cudaGetDevice(&was_) != cudaSuccess) was_ = -1;
+    ok_ = was_ == device || cudaSetDevice(device) == cudaSuccess;
+    if (was_ == device) was_ = -1;
+  }
+  ~DeviceGuard() {
+    if (was_ >= 0) cudaSetDevice(was_);
+  }
+  bool ok() const { return ok_; }
+
+ private:
+  int was_ = -1;
+  bool ok_ = false;
+};
+
+}  // namespace duolm

@@ -1,0 +1,523 @@
+// Paged KV cache: the plan of a batch, and the step that fills the cache from
+// the projections (QK-norm, rotary positions, K and V into their pages).
+#include "pages.cuh"
+
+namespace duolm {
+
+PagesPath pages_path(int dtype, int64_t max_rows, int group) {
+  return max_rows * group <= 16 ? kPathSimt16 : kPathSimt64;
+}
+
+PathShape pages_path_shape(PagesPath path, int head_dim) {
+  PathShape sh{};
+  sh.slots = path == kPathSimt16 ? 16 : 64;
+  sh.keys = 64;
+  sh.part_words = sh.slots * (head_dim + 2);
+  return sh;
+}
+
+int64_t pages_plan_layout(char* base, int64_t n, int64_t n_rows, int n_kv_heads, int group, PathShape sh, int ctas,
+                          PagesPlan* out) {
+  const int64_t tokens = sh.slots / group;  // of one item
+  const int64_t max_items = n_kv_heads * (n + n_rows / tokens);
+  if (max_items >= kScanCap) return -1;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += (bytes + 127) / 128 * 128;
+    return base + o;
+  };
+  PagesPlan pl;
+  pl.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
+  pl.cta_item = reinterpret_cast<int32_t*>(take(4 * ctas));
+  pl.arrived = reinterpret_cast<int32_t*>(take(4 * max_items));
+  pl.items = reinterpret_cast<PageItem*>(take((int64_t)sizeof(PageItem) * max_items));
+  pl.base = reinterpret_cast<int2*>(take(8 * n));
+  pl.rows = reinterpret_cast<int2*>(take(8 * n_rows));
+  pl.parts = reinterpret_cast<float*>(take(2ll * ctas * sh.part_words * 4));
+  pl.max_items = (int)max_items;
+  pl.ctas = ctas;
+  if (out) *out = pl;
+  return at;
+}
+
+namespace {
+
+struct BatchView {
+  const int32_t* seq;
+  const int32_t* offset;
+  int n, n_rows, group, causal;
+};
+
+// An entry's query rows and length; false (and the flag) where they are out
+// of range.
+__device__ __forceinline__ bool entry_of(const PagesView& p, const BatchView& b, int i, int* s, int* o, int* rows,
+                                         int* len, uint32_t* err) {
+  *s = b.seq[i];
+  *o = b.offset[i];
+  const int e = b.offset[i + 1];
+  *rows = 0;
+  *len = 0;
+  if ((unsigned)*s >= (unsigned)p.n_seqs) {
+    *err = ERR_BAD_SEQ;
+    return false;
+  }
+  const int l = p.length[*s];
+  if (*o < 0 || e < *o || e > b.n_rows || l < 0 || l > p.max_tokens()) {
+    *err = ERR_BAD_LENGTH;
+    return false;
+  }
+  *rows = e - *o;
+  *len = l;
+  return true;
+}
+
+// key tiles of the query rows [r0, r0 + m) of an entry (one at least: an item
+// that sees no key still writes its rows)
+__device__ __forceinline__ int item_keys(const BatchView& b, int rows, int len, int r0, int m) {
+  return b.causal ? max(0, len - rows + min(r0 + m, rows)) : len;
+}
+
+// CTA 0: the attention's items and how the CTAs divide their key tiles.  The
+// other CTAs: where each query row's token lies in the cache.
+__global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, BatchView b, PagesPlan pl, int m,
+                                                                  int keys) {
+  extern __shared__ uint32_t seen[];
+  __shared__ int s_scan[32];
+  __shared__ uint32_t s_err;
+  pdl_launch_dependents();
+  if (blockIdx.x > 0) {
+    pdl_wait();
+    if (pages_raised(p)) return;
+    for (int r = (blockIdx.x - 1) * kPlanThreads + threadIdx.x; r < b.n_rows; r += (gridDim.x - 1) * kPlanThreads) {
+      // the last entry that begins at or before r
+      int lo = 0, hi = b.n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (b.offset[mid] <= r)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      int s, o, rows, len;
+      uint32_t err;
+      int2 at = make_int2(kRowNone, 0);
+      if (entry_of(p, b, lo, &s, &o, &rows, &len, &err) && r >= o && r < o + rows) {
+        const int pos = len - rows + r - o;
+        at.x = kRowOutside;
+        if (pos >= 0) {
+          const int page = p.table[(int64_t)s * p.max_pages + (pos >> p.page_shift)];
+          if ((unsigned)page < (unsigned)p.n_pages)
+            at = make_int2((page << p.page_shift) + (pos & (p.page_tokens - 1)), pos);
+          else
+            raise_error(p.st, ERR_BAD_INDEX, 88);
+        }
+      }
+      pl.rows[r] = at;
+    }
+    return;
+  }
+  for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
+  if (threadIdx.x == 0) s_err = 0;
+  __syncthreads();
+  pdl_wait();
+  if (pages_raised(p)) return;
+  int items = 0, units = 0;
+  for (int i0 = 0; i0 < b.n; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    int n_it = 0, n_un = 0;
+    if (i < b.n) {
+      int s, o, rows, len;
+      uint32_t err = 0;
+      const bool ok = entry_of(p, b, i, &s, &o, &rows, &len, &err);
+      if (!ok || (i == 0 && o != 0)) {
+        atomicOr(&s_err, ok ? (uint32_t)ERR_BAD_LENGTH : err);
+      } else if (!claim(seen, s)) {
+        atomicOr(&s_err, ERR_BAD_SEQ);
+      } else {
+        const int tiles = (rows + m - 1) / m;
+        int64_t u = 0;
+        for (int t = 0; t < tiles; ++t) u += max(1, (item_keys(b, rows, len, t * m, m) + keys - 1) / keys);
+        n_it = tiles * p.n_kv_heads;
+        n_un = (int)min(u * p.n_kv_heads, (int64_t)kScanCap);
+      }
+    }
+    int all_it, all_un;
+    const int it = block_scan(n_it, s_scan, &all_it), un = block_scan(n_un, s_scan, &all_un);
+    if (i < b.n) pl.base[i] = make_int2(items + it, units + un);
+    items = min(items + all_it, kScanCap);
+    units = min(units + all_un, kScanCap);
+  }
+  __syncthreads();
+  if (s_err || units >= kScanCap || items > pl.max_items) {
+    if (threadIdx.x == 0) {
+      raise_error(p.st, s_err ? s_err : (uint32_t)ERR_BAD_LENGTH, 86);
+      pl.head->n_items = 0;
+      pl.head->units = pl.head->ctas = 0;
+    }
+    return;
+  }
+  const int ctas = min(pl.ctas, units);
+  if (threadIdx.x == 0) {
+    pl.head->n_items = items;
+    pl.head->units = units;
+    pl.head->ctas = ctas;
+  }
+  for (int i = threadIdx.x; i < items; i += kPlanThreads) pl.arrived[i] = 0;
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < b.n; i += kPlanThreads / 32) {
+    int s, o, rows, len;
+    uint32_t err;
+    entry_of(p, b, i, &s, &o, &rows, &len, &err);
+    const int2 base = pl.base[i];
+    const int tiles = (rows + m - 1) / m;
+    int per_head = 0;  // units of one head's items
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+      const int t = t0 + lane;
+      int u = t < tiles ? max(1, (item_keys(b, rows, len, t * m, m) + keys - 1) / keys) : 0;
+#pragma unroll
+      for (int o2 = 16; o2 > 0; o2 >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o2);
+      per_head += u;
+    }
+    int before = 0;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+      const int t = t0 + lane;
+      const int nk = t < tiles ? item_keys(b, rows, len, t * m, m) : 0;
+      const int u = t < tiles ? max(1, (nk + keys - 1) / keys) : 0;
+      int x = u;
+#pragma unroll
+      for (int o2 = 1; o2 < 32; o2 <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o2);
+        if (lane >= o2) x += y;
+      }
+      if (t < tiles)
+        for (int h = 0; h < p.n_kv_heads; ++h) {
+          PageItem it;
+          it.seq = s;
+          it.kv_head = h;
+          it.row0 = o + t * m;
+          it.n_rows = min(m, rows - t * m);
+          it.last0 = b.causal ? len - rows + t * m : 0;
+          it.n_keys = nk;
+          it.unit0 = base.y + h * per_head + before + x - u;
+          it.n_tiles = u;
+          const int k = base.x + h * tiles + t;
+          pl.items[k] = it;
+          // CTAs whose first unit is in this item
+          for (int c = unit_cta(it.unit0, units, ctas); c < ctas; ++c) {
+            const int first = cta_unit(c, units, ctas);
+            if (first >= it.unit0 + u) break;
+            if (first >= it.unit0) pl.cta_item[c] = k;
+          }
+        }
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// write: per row, RMSNorm over each q and k head with its gain, rotation of
+// the pairs (i, i + hd/2) by the row's position, q to q_out, K and V to the
+// row's slot.  One pass: a head's two halves sit in SEG lanes, 16 bytes of
+// each half to a lane, so the pairs of the rotation are in one lane and the
+// sum of squares is a shuffle within SEG; sums and rotation in fp32, one
+// rounding at the end.  A warp keeps the row's angles in registers over
+// U x (32 / SEG) heads.  Bound by HBM (each row read and written once).
+// ---------------------------------------------------------------------------
+struct WriteArgs {
+  const char *q, *k, *v;
+  char* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const float *q_gain, *k_gain;
+  const float2* rope;
+  int rope_positions;
+  int n_q_heads, n_rows, layer;
+  float eps;
+};
+
+template <typename T>
+__device__ __forceinline__ float elem_f32(T x);
+template <>
+__device__ __forceinline__ float elem_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float elem_f32<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float elem_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T f32_elem(float x);
+template <>
+__device__ __forceinline__ float f32_elem<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half f32_elem<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 f32_elem<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+template <typename T, int SEG, int U>
+__global__ void __launch_bounds__(256) pages_write_kernel(PagesView p, PagesPlan pl, WriteArgs a) {
+  constexpr int E = 16 / sizeof(T);   // elements of a 16-byte word
+  constexpr int HPW = 32 / SEG;       // heads a warp holds at a time
+  pdl_launch_dependents();
+  pdl_wait();
+  if (pages_raised(p)) return;
+  const int lane = threadIdx.x & 31, seg = lane / SEG, sl = lane % SEG;
+  const int half = p.head_dim / 2;
+  const bool in = sl * E < half;  // head_dim / 2 below SEG words: idle lanes
+  const int n_heads = (a.q ? a.n_q_heads : 0) + 2 * p.n_kv_heads, q_heads = n_heads - 2 * p.n_kv_heads;
+  const int groups = (n_heads + U * HPW - 1) / (U * HPW);
+  const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5, warps = (gridDim.x * (int64_t)blockDim.x) >> 5;
+  const float inv_hd = 1.f / p.head_dim;
+  for (int64_t w = warp; w < (int64_t)a.n_rows * groups; w += warps) {
+    const int row = (int)(w / groups), h0 = (int)(w % groups) * (U * HPW);
+    const int2 at = pl.rows[row];
+    if (at.x == kRowNone) continue;
+    if (at.x < 0 || (a.rope && at.y >= a.rope_positions)) {
+      raise_error(p.st, ERR_BAD_LENGTH, 87);
+      continue;
+    }
+    uint4 lo[U], hi[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * HPW + seg;
+      if (h >= n_heads || !in) continue;
+      const char* src;
+      if (h < q_heads)
+        src = a.q + ((int64_t)row * a.q_stride + (int64_t)h * p.head_dim) * sizeof(T);
+      else if (h < q_heads + p.n_kv_heads)
+        src = a.k + ((int64_t)row * a.k_stride + (int64_t)(h - q_heads) * p.head_dim) * sizeof(T);
+      else
+        src = a.v + ((int64_t)row * a.v_stride + (int64_t)(h - q_heads - p.n_kv_heads) * p.head_dim) * sizeof(T);
+      lo[u] = __ldcs(reinterpret_cast<const uint4*>(src) + sl);
+      hi[u] = __ldcs(reinterpret_cast<const uint4*>(src + half * sizeof(T)) + sl);
+    }
+    float c[E], s[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) c[e] = 1.f, s[e] = 0.f;
+    if (a.rope && in) {
+      const float4* r = reinterpret_cast<const float4*>(a.rope + (int64_t)at.y * half + sl * E);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const float4 x = r[e];
+        c[2 * e] = x.x, s[2 * e] = x.y, c[2 * e + 1] = x.z, s[2 * e + 1] = x.w;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * HPW + seg;
+      const bool mine = h < n_heads && in;
+      const bool is_q = h < q_heads, is_v = h >= q_heads + p.n_kv_heads;
+      float x[2 * E];
+      float ss = 0.f;
+      if (mine) {
+        const T* l = reinterpret_cast<const T*>(&lo[u]);
+        const T* g = reinterpret_cast<const T*>(&hi[u]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = elem_f32<T>(l[e]), x[E + e] = elem_f32<T>(g[e]);
+#pragma unroll
+        for (int e = 0; e < 2 * E; ++e) ss += x[e] * x[e];
+      }
+#pragma unroll
+      for (int o = SEG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (!mine) continue;
+      if (!is_v) {
+        const float* gain = is_q ? a.q_gain : a.k_gain;
+        if (gain) {
+          const float r = rsqrtf(ss * inv_hd + a.eps);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            x[e] *= r * gain[sl * E + e];
+            x[E + e] *= r * gain[half + sl * E + e];
+          }
+        }
+        T* l = reinterpret_cast<T*>(&lo[u]);
+        T* g = reinterpret_cast<T*>(&hi[u]);
+        if (a.rope || gain) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            l[e] = f32_elem<T>(x[e] * c[e] - x[E + e] * s[e]);
+            g[e] = f32_elem<T>(x[E + e] * c[e] + x[e] * s[e]);
+          }
+        }
+      }
+      char* dst;
+      if (is_q) {
+        dst = a.q_out + ((int64_t)row * a.q_out_stride + (int64_t)h * p.head_dim) * sizeof(T);
+      } else {
+        const int kh = h - q_heads - (is_v ? p.n_kv_heads : 0);
+        const int64_t page = at.x >> p.page_shift;
+        dst = (is_v ? p.v : p.k) + a.layer * p.layer_bytes() + page * p.page_bytes() + kh * p.head_bytes() +
+              (int64_t)(at.x & (p.page_tokens - 1)) * p.head_dim * sizeof(T);
+      }
+      reinterpret_cast<uint4*>(dst)[sl] = lo[u];
+      reinterpret_cast<uint4*>(dst + half * sizeof(T))[sl] = hi[u];
+    }
+  }
+}
+
+template <typename T, int SEG>
+cudaError_t write_seg(const PagesView& p, const PagesPlan& pl, const WriteArgs& a, int sms, cudaStream_t s) {
+  constexpr int HPW = 32 / SEG, U = 4;
+  const int n_heads = (a.q ? a.n_q_heads : 0) + 2 * p.n_kv_heads;
+  // four heads in flight per lane once that still gives every SM 16 warps;
+  // below, one, so that few rows spread over more warps
+  const int64_t wide = (int64_t)a.n_rows * ((n_heads + U * HPW - 1) / (U * HPW));
+  if (wide >= 16ll * sms) {
+    const int grid = (int)std::min<int64_t>((wide + 7) / 8, 8ll * sms);
+    return launch_ex(pages_write_kernel<T, SEG, U>, dim3(grid), dim3(256), 0, s, true, p, pl, a);
+  }
+  const int64_t narrow = (int64_t)a.n_rows * ((n_heads + HPW - 1) / HPW);
+  const int grid = (int)std::min<int64_t>((narrow + 7) / 8, 8ll * sms);
+  return launch_ex(pages_write_kernel<T, SEG, 1>, dim3(grid), dim3(256), 0, s, true, p, pl, a);
+}
+
+// What the host can check of a batch.
+int batch_check(const PagesView& p, const duolm_pages_batch* b) {
+  if (!b) return pages_fail(DUOLM_E_ARG, "null batch");
+  if (b->n < 0 || b->n_rows < 0 || b->max_rows < 0 || b->n_q_heads < 1 || b->n_q_heads % p.n_kv_heads)
+    return pages_fail(DUOLM_E_ARG, "batch: a size out of range, or query heads not a multiple of KV heads");
+  if (b->n_q_heads / p.n_kv_heads > 64) return pages_fail(DUOLM_E_ARG, "batch: more than 64 query heads per KV head");
+  if (b->n > p.n_seqs) return pages_fail(DUOLM_E_ARG, "batch: %d entries for %d sequences (one each)", b->n, p.n_seqs);
+  if ((int64_t)b->n_rows * b->n_q_heads > INT32_MAX)
+    return pages_fail(DUOLM_E_CAPACITY, "batch: 2^31 query rows x heads and more");
+  if (b->n == 0 || b->n_rows == 0) return 0;
+  if (!b->seq || !b->offset || !b->plan) return pages_fail(DUOLM_E_ARG, "batch: null array");
+  if (reinterpret_cast<uintptr_t>(b->plan) & 127) return pages_fail(DUOLM_E_ARG, "batch: plan not 128-byte aligned");
+  return 0;
+}
+
+// Where the parts of a checked batch's plan lie.
+int batch_layout(const duolm_pages* pages, const PagesView& p, const duolm_pages_batch* b, PagesPlan* pl,
+                 PagesPath* path, int* sms) {
+  *sms = pages_sms(pages->device);
+  if (!*sms) return pages_fail(DUOLM_E_CUDA, "device %d", pages->device);
+  const int group = b->n_q_heads / p.n_kv_heads;
+  *path = pages_path(pages->dtype, b->max_rows, group);
+  const int64_t need = pages_plan_layout(static_cast<char*>(b->plan), b->n, b->n_rows, p.n_kv_heads, group,
+                                         pages_path_shape(*path, p.head_dim), *sms, pl);
+  if (need < 0) return pages_fail(DUOLM_E_CAPACITY, "batch: too many items");
+  if (b->plan_bytes < need)
+    return pages_fail(DUOLM_E_CAPACITY, "plan of %lld bytes, %lld needed", (long long)b->plan_bytes, (long long)need);
+  return 0;
+}
+
+bool misaligned(const void* p, int64_t stride, int elem) {
+  return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * elem)) & 15;
+}
+
+}  // namespace
+}  // namespace duolm
+
+using namespace duolm;
+
+extern "C" int64_t duolm_pages_plan_bytes(const duolm_pages* pages, int n, int n_rows, int max_rows, int n_q_heads) {
+  PagesView p;
+  if (const int rc = pages_view(pages, &p)) return rc;
+  if (n < 0 || n_rows < 0 || max_rows < 0 || n_q_heads < 1 || n_q_heads % p.n_kv_heads || n_q_heads / p.n_kv_heads > 64)
+    return pages_fail(DUOLM_E_ARG, "pages_plan_bytes: a size out of range");
+  const int sms = pages_sms(pages->device);
+  if (!sms) return pages_fail(DUOLM_E_CUDA, "pages_plan_bytes: device %d", pages->device);
+  const int group = n_q_heads / p.n_kv_heads;
+  const int64_t need = pages_plan_layout(nullptr, n, n_rows, p.n_kv_heads, group,
+                                         pages_path_shape(pages_path(pages->dtype, max_rows, group), p.head_dim), sms,
+                                         nullptr);
+  return need < 0 ? pages_fail(DUOLM_E_CAPACITY, "pages_plan_bytes: too many items") : need;
+}
+
+extern "C" int duolm_pages_plan(const duolm_pages* pages, const duolm_pages_batch* batch, void* cuda_stream) {
+  PagesView p;
+  PagesPlan pl;
+  PagesPath path;
+  int sms, rc;
+  if ((rc = pages_view(pages, &p)) || (rc = batch_check(p, batch))) return rc;
+  if (batch->n == 0 || batch->n_rows == 0) return 0;
+  if ((rc = batch_layout(pages, p, batch, &pl, &path, &sms))) return rc;
+  DeviceGuard g(pages->device);
+  if (!g.ok()) return pages_fail(DUOLM_E_CUDA, "pages_plan: device %d", pages->device);
+  const int group = batch->n_q_heads / p.n_kv_heads;
+  const PathShape sh = pages_path_shape(path, p.head_dim);
+  const BatchView b{batch->seq, batch->offset, batch->n, batch->n_rows, group, batch->causal != 0};
+  const size_t smem = (size_t)((p.n_seqs + 31) / 32) * 4;
+  const int grid = 1 + std::min((batch->n_rows + kPlanThreads - 1) / kPlanThreads, sms - 1);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024 - 512)
+    e = cudaFuncSetAttribute(batch_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  if (e == cudaSuccess)
+    e = launch_ex(batch_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(cuda_stream), true,
+                  p, b, pl, sh.slots / group, sh.keys);
+  return e == cudaSuccess ? 0 : pages_fail(DUOLM_E_CUDA, "pages_plan: %s", cudaGetErrorString(e));
+}
+
+extern "C" int duolm_pages_write(const duolm_pages* pages, const duolm_pages_batch* batch, int layer, const void* q,
+                                 int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                 const float* q_gain, const float* k_gain, float eps, const float* rope,
+                                 int64_t rope_positions, void* q_out, int64_t q_out_stride, void* cuda_stream) {
+  PagesView p;
+  PagesPlan pl;
+  PagesPath path;
+  int sms, rc;
+  if ((rc = pages_view(pages, &p)) || (rc = batch_check(p, batch))) return rc;
+  if (layer < 0 || layer >= p.n_layers) return pages_fail(DUOLM_E_ARG, "pages_write: layer %d", layer);
+  if (batch->n == 0 || batch->n_rows == 0) return 0;
+  if (!k || !v || (q && !q_out)) return pages_fail(DUOLM_E_ARG, "pages_write: null array");
+  const int64_t kd = (int64_t)p.n_kv_heads * p.head_dim, qd = (int64_t)batch->n_q_heads * p.head_dim;
+  if (k_stride < kd || v_stride < kd || (q && (q_stride < qd || q_out_stride < qd)))
+    return pages_fail(DUOLM_E_ARG, "pages_write: a row stride below the row's elements");
+  if (misaligned(k, k_stride, p.elem) || misaligned(v, v_stride, p.elem) ||
+      (q && (misaligned(q, q_stride, p.elem) || misaligned(q_out, q_out_stride, p.elem))) ||
+      (reinterpret_cast<uintptr_t>(rope) & 15))
+    return pages_fail(DUOLM_E_ARG, "pages_write: rows and the rotation table must be 16-byte aligned");
+  if (rope && rope_positions < 1) return pages_fail(DUOLM_E_ARG, "pages_write: empty rotation table");
+  if (!(eps >= 0.f)) return pages_fail(DUOLM_E_ARG, "pages_write: eps %g", eps);
+  if ((rc = batch_layout(pages, p, batch, &pl, &path, &sms))) return rc;
+  DeviceGuard g(pages->device);
+  if (!g.ok()) return pages_fail(DUOLM_E_CUDA, "pages_write: device %d", pages->device);
+  const WriteArgs a{static_cast<const char*>(q), static_cast<const char*>(k), static_cast<const char*>(v),
+                    static_cast<char*>(q_out), q_stride, k_stride, v_stride, q_out_stride, q_gain, k_gain,
+                    reinterpret_cast<const float2*>(rope), (int)std::min<int64_t>(rope_positions, INT32_MAX),
+                    batch->n_q_heads, batch->n_rows, layer, eps};
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const int words = p.head_dim * p.elem / 32;  // 16-byte words of half a head
+  auto run = [&](auto zero) -> cudaError_t {
+    using T = decltype(zero);
+    if (words <= 4) return write_seg<T, 4>(p, pl, a, sms, s);
+    if (words <= 8) return write_seg<T, 8>(p, pl, a, sms, s);
+    if constexpr (sizeof(T) == 4) {
+      if (words <= 16) return write_seg<T, 16>(p, pl, a, sms, s);
+      return write_seg<T, 32>(p, pl, a, sms, s);
+    }
+    return cudaErrorInvalidValue;
+  };
+  cudaError_t e;
+  if (pages->dtype == DUOLM_DTYPE_FP32)
+    e = run(0.f);
+  else if (pages->dtype == DUOLM_DTYPE_FP16)
+    e = run(__half{});
+  else
+    e = run(__nv_bfloat16{});
+  return e == cudaSuccess ? 0 : pages_fail(DUOLM_E_CUDA, "pages_write: %s", cudaGetErrorString(e));
+}
+
+extern "C" int duolm_pages_attention(const duolm_pages* pages, const duolm_pages_batch* batch, int layer,
+                                     const void* q, int64_t q_stride, float scale, void* out, int64_t out_stride,
+                                     float* lse, void* cuda_stream) {
+  PagesView p;
+  PagesPlan pl;
+  PagesPath path;
+  int sms, rc;
+  if ((rc = pages_view(pages, &p)) || (rc = batch_check(p, batch))) return rc;
+  if (layer < 0 || layer >= p.n_layers) return pages_fail(DUOLM_E_ARG, "pages_attention: layer %d", layer);
+  if (!(scale > 0.f) || scale > 1e30f) return pages_fail(DUOLM_E_ARG, "pages_attention: scale %g", scale);
+  if (batch->n == 0 || batch->n_rows == 0) return 0;
+  if (!q || !out) return pages_fail(DUOLM_E_ARG, "pages_attention: null array");
+  const int64_t qd = (int64_t)batch->n_q_heads * p.head_dim;
+  if (q_stride < qd || out_stride < qd)
+    return pages_fail(DUOLM_E_ARG, "pages_attention: a row stride below the row's elements");
+  if (misaligned(q, q_stride, p.elem) || misaligned(out, out_stride, p.elem))
+    return pages_fail(DUOLM_E_ARG, "pages_attention: rows must be 16-byte aligned");
+  if ((rc = batch_layout(pages, p, batch, &pl, &path, &sms))) return rc;
+  DeviceGuard g(pages->device);
+  if (!g.ok()) return pages_fail(DUOLM_E_CUDA, "pages_attention: device %d", pages->device);
+  const AttnArgs a{static_cast<const char*>(q), static_cast<char*>(out), lse, q_stride, out_stride, batch->n_q_heads,
+                   batch->n_q_heads / p.n_kv_heads, batch->causal != 0, layer, scale};
+  const cudaError_t e = pages_attention_simt(p, pl, a, pages->dtype, path == kPathSimt16, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? 0 : pages_fail(DUOLM_E_CUDA, "pages_attention: %s", cudaGetErrorString(e));
+}
