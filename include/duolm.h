@@ -464,7 +464,9 @@ int duolm_pages_compact(const duolm_pages *pages, int32_t *table_out, int32_t *r
 /* Wait for cuda_stream, report what the device raised since the last check
  * and clear it: DUOLM_E_CAPACITY (too few free pages), DUOLM_E_ARG (a
  * sequence, length, offset or position out of range), DUOLM_E_DEVICE (a page
- * id out of range, a wait that ran out).  Not inside a capture. */
+ * id out of range, a wait that ran out), DUOLM_E_STATE (a write or attention
+ * on a plan that was made for a batch of other sizes, or that an error cut
+ * short: plan the batch again).  Not inside a capture. */
 int duolm_pages_check(const duolm_pages *pages, void *cuda_stream);
 
 /*

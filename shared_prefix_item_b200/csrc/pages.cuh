@@ -23,6 +23,7 @@ enum : uint32_t {  // further bits of the cache's status word
   ERR_NO_PAGES = 8u,     // fewer free pages than the call needs
   ERR_BAD_SEQ = 16u,     // a sequence id out of range, twice in a call, or in the wrong state
   ERR_BAD_LENGTH = 32u,  // a length, token count or offset out of range
+  ERR_STALE_PLAN = 64u,  // a plan on which an earlier call was cut short
 };
 
 struct PagesView {
@@ -41,9 +42,10 @@ struct PagesView {
   __host__ __device__ int max_tokens() const { return max_pages << page_shift; }
 };
 
-// Read once per kernel, after pdl_wait().
+// Read once per kernel, after pdl_wait(), by every thread of the block:
+// the same answer in every thread of the block, whatever other blocks raise meanwhile
 __device__ __forceinline__ bool pages_raised(const PagesView& p) {
-  return *reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0;
+  return __syncthreads_or(*reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0);
 }
 
 // ---- one CTA deciding for a whole call ----------------------------------------
@@ -114,11 +116,20 @@ inline PagesWork pages_work(void* ws, int64_t n_pages, int64_t n_seqs) {
 
 // ---- batch plan --------------------------------------------------------------
 // Which kernel reads the batch, decided by the host from sizes alone.
-enum PagesPath { kPathSimt16 = 0, kPathSimt64 = 1 };
+enum PagesPath {
+  kPathSimt16,  // fp32, up to 16 (token, query head) rows per KV head
+  kPathSimt64,  // fp32
+  kPathFew,     // 16-bit, up to 16 rows per KV head: bound by reading K and V
+  kPathTc       // 16-bit, tcgen05
+};
 struct PathShape {
-  int slots;     // (token, query head) rows of one item
-  int keys;      // keys of one tile
-  int part_words;  // fp32 words of one partial result: slots x (head_dim + 2)
+  int slots;       // (token, query head) rows of one sub-tile
+  int subs;        // sub-tiles of one item
+  int keys;        // keys of one tile
+  int grain;       // tiles of one unit in a batch too small to fill the CTAs for long (else 1)
+  int ctas_per_sm;
+  int part_words;  // fp32 words of one partial result: subs x slots x (head_dim + 2)
+  int tokens(int group) const { return subs * (slots / group); }  // of one item
 };
 PagesPath pages_path(int dtype, int64_t max_rows, int group);
 PathShape pages_path_shape(PagesPath path, int head_dim);
@@ -128,7 +139,7 @@ PathShape pages_path_shape(PagesPath path, int head_dim);
 // when causal, [0, n_keys) otherwise.
 struct PageItem {
   int seq, kv_head, row0, n_rows;
-  int last0, n_keys, unit0, n_tiles;  // unit0: key tiles of all items before it
+  int last0, n_keys, unit0, n_tiles;  // unit0: units of all items before it
 };
 static_assert(sizeof(PageItem) == 32, "item layout");
 
@@ -137,9 +148,13 @@ constexpr int kRowOutside = -2;  // more rows than the sequence has tokens: nowh
 
 struct PlanHead {
   int n_items;
-  int units;  // key tiles of all items; CTA c of n takes [c units / n, (c + 1) units / n)
+  int units;  // of all items, each `grain` key tiles (an item's last may have fewer); CTA c of n takes
+              // [c units / n, (c + 1) units / n)
   int ctas;   // CTAs that take part: all, or one per unit where there are fewer
-  int pad[13];
+  int stale;  // a call on this plan was cut short: its counts of arrived parts are void
+  uint32_t key;  // what it was made for (PagesPlan::key)
+  int grain;
+  int pad[10];
 };
 struct PagesPlan {
   PlanHead* head;
@@ -150,6 +165,7 @@ struct PagesPlan {
   int2* rows;         // [n_rows] {page * page_tokens + slot, position}; x: kRowNone, kRowOutside
   float* parts;       // [2 ctas][part_words]
   int max_items, ctas;
+  uint32_t key;       // of the sizes that the plan's contents go by: a plan made for others, or none, is refused
 };
 // Layout of a plan for n entries and n_rows query rows; returns its bytes.
 int64_t pages_plan_layout(char* base, int64_t n, int64_t n_rows, int n_kv_heads, int group, PathShape sh, int ctas,
@@ -169,16 +185,65 @@ __host__ __device__ inline int unit_cta(int64_t u, int64_t units, int ctas) {
 // result does not depend on the order of arrival.  A CTA holds at most two
 // parts: slot 2c for an item begun before it, 2c + 1 for one begun by it.
 struct CtaWork {  // a CTA's units [unit, end), the first of them in item `item`
-  int unit, end, item, units, ctas;
+  int unit, end, item, units, ctas, grain;
 };
 __device__ __forceinline__ CtaWork cta_work(const PagesPlan& pl, int cta) {
-  CtaWork w{0, 0, 0, pl.head->units, pl.head->ctas};
+  CtaWork w{0, 0, 0, pl.head->units, pl.head->ctas, pl.head->grain};
   if (pl.head->n_items == 0 || cta >= w.ctas) return w;
   w.unit = cta_unit(cta, w.units, w.ctas);
   w.end = cta_unit(cta + 1, w.units, w.ctas);
   w.item = pl.cta_item[cta];
   return w;
 }
+// A CTA's items in order, the next one's record already on its way.  Every
+// role of a kernel walks them by itself.
+struct ItemWalk {
+  const PageItem* items;
+  CtaWork w;
+  PageItem next_item;
+  int index;   // of the item next() gave last
+  int t0, t1;  // its key tiles that are this CTA's
+  __device__ ItemWalk(const PagesPlan& pl, int cta) : items(pl.items), w(cta_work(pl, cta)) {
+    if (w.unit < w.end) next_item = items[w.item];
+  }
+  __device__ bool next(PageItem* it) {
+    if (w.unit >= w.end) return false;
+    *it = next_item;
+    index = w.item++;
+    const int end = min(it->unit0 + units_of(*it), w.end);
+    t0 = (w.unit - it->unit0) * w.grain;
+    t1 = min(it->n_tiles, (end - it->unit0) * w.grain);
+    w.unit = end;
+    if (w.unit < w.end) next_item = items[w.item];
+    return true;
+  }
+  __device__ int units_of(const PageItem& it) const { return (it.n_tiles + w.grain - 1) / w.grain; }
+  // the CTAs that share the item
+  __device__ int first_cta(const PageItem& it) const { return unit_cta(it.unit0, w.units, w.ctas); }
+  __device__ int last_cta(const PageItem& it) const { return unit_cta(it.unit0 + units_of(it) - 1, w.units, w.ctas); }
+  __device__ bool whole(const PageItem& it) const { return t0 == 0 && t1 == it.n_tiles; }
+};
+
+// Whether this call may run on the plan (the same answer in every thread of
+// the block): not while the cache's status is raised, not on a plan that such
+// a call was cut short on, and not on a buffer that holds no plan for these
+// sizes.
+__device__ __forceinline__ bool plan_usable(const PagesView& p, const PagesPlan& pl) {
+  if (pages_raised(p)) {
+    if (threadIdx.x == 0) pl.head->stale = 1;
+    return false;
+  }
+  if (__syncthreads_or(*reinterpret_cast<volatile const int*>(&pl.head->stale) != 0 || pl.head->key != pl.key)) {
+    if (threadIdx.x == 0) raise_error(p.st, ERR_STALE_PLAN, 89);
+    return false;
+  }
+  return true;
+}
+__device__ __forceinline__ void raise_on_plan(const PagesView& p, const PagesPlan& pl, uint32_t flag, uint32_t where) {
+  pl.head->stale = 1;
+  raise_error(p.st, flag, where);
+}
+
 __device__ __forceinline__ float* part_of(const PagesPlan& pl, int part_words, int cta, bool begun_here) {
   return pl.parts + (int64_t)(2 * cta + (begun_here ? 1 : 0)) * part_words;
 }
@@ -192,8 +257,11 @@ struct AttnArgs {
   int n_q_heads, group, causal, layer;
   float scale;
 };
-cudaError_t pages_attention_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, int dtype, bool few,
-                                 cudaStream_t s);
+cudaError_t pages_attention_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool few, cudaStream_t s);
+// 16-bit elements (pages_attention_few.cu, pages_attention_tc.cu); n_rows: rows of q
+cudaError_t pages_attention_few(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, cudaStream_t s);
+cudaError_t pages_attention_tc(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, int n_rows,
+                               cudaStream_t s);
 
 // host helpers (pages.cu)
 int pages_fail(int code, const char* fmt, ...);

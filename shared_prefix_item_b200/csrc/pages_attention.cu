@@ -1,5 +1,5 @@
-// Attention of a chunk of query rows over a paged KV cache, on CUDA cores
-// with fp32 operands.
+// Attention of a chunk of query rows over a paged KV cache: the fp32 path, on
+// CUDA cores (the tensor cores have no fp32 operands).
 //
 // One pass over the keys with a running maximum and sum: for a tile of 64
 // keys, s = q.k scale (base 2), m' = max(m, max s), p = 2^(s - m'),
@@ -18,39 +18,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 64;
 
-template <typename T>
-struct Conv;
-template <>
-struct Conv<float> {
-  static __device__ float in(float x) { return x; }
-  static __device__ float out(float x) { return x; }
-};
-template <>
-struct Conv<__half> {
-  static __device__ float in(__half x) { return __half2float(x); }
-  static __device__ __half out(float x) { return __float2half_rn(x); }
-};
-template <>
-struct Conv<__nv_bfloat16> {
-  static __device__ float in(__nv_bfloat16 x) { return __bfloat162float(x); }
-  static __device__ __nv_bfloat16 out(float x) { return __float2bfloat16_rn(x); }
-};
-
-// 16 bytes of T as fp32 to shared memory
-template <typename T>
-__device__ __forceinline__ void put_words(float* dst, uint4 w) {
-  const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) dst[i] = Conv<T>::in(e[i]);
-}
-
 }  // namespace
 
 // M: slots of an item; NC: head_dim / 16, rounded up to what is instantiated
-template <typename T, int M, int NC>
+template <int M, int NC>
 __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, PagesPlan pl, AttnArgs a) {
   constexpr int RM = M / 16;
-  constexpr int E = 16 / sizeof(T);
+  constexpr int E = 4;
   extern __shared__ float smem[];
   __shared__ int s_last;
   const int hd = p.head_dim, ld = hd + 4, nc = hd / 16, words = hd / E;
@@ -60,27 +34,25 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
   float* Ps = Vs + kTile * hd;
   pdl_launch_dependents();
   pdl_wait();
-  if (pages_raised(p)) return;
+  if (!plan_usable(p, pl)) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int G = a.group, cta = blockIdx.x;
   const float scale2 = a.scale * 1.4426950408889634f;
-  const int64_t layer_elems = p.layer_bytes() / sizeof(T), page_elems = p.page_bytes() / sizeof(T),
-                head_elems = p.head_bytes() / sizeof(T);
-  const T* kbase = reinterpret_cast<const T*>(p.k) + a.layer * layer_elems;
-  const T* vbase = reinterpret_cast<const T*>(p.v) + a.layer * layer_elems;
-  CtaWork w = cta_work(pl, cta);
-  for (; w.unit < w.end; ++w.item) {
-    const PageItem it = pl.items[w.item];
-    const int t0 = w.unit - it.unit0, t1 = min(it.n_tiles, w.end - it.unit0);
-    w.unit += t1 - t0;
+  const int64_t layer_elems = p.layer_bytes() / 4, page_elems = p.page_bytes() / 4,
+                head_elems = p.head_bytes() / 4;
+  const float* kbase = reinterpret_cast<const float*>(p.k) + a.layer * layer_elems;
+  const float* vbase = reinterpret_cast<const float*>(p.v) + a.layer * layer_elems;
+  PageItem it;
+  for (ItemWalk walk(pl, cta); walk.next(&it);) {
+    const int t0 = walk.t0, t1 = walk.t1;
     __syncthreads();  // the previous item's shared tiles are done with
     for (int i = tid; i < M * words; i += kThreads) {
       const int r = i / words, c = i % words, j = r / G;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (j < it.n_rows)
-        x = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + (int64_t)(it.row0 + j) * a.q_stride +
+        x = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(a.q) + (int64_t)(it.row0 + j) * a.q_stride +
                                             (int64_t)(it.kv_head * G + r % G) * hd + c * E);
-      put_words<T>(Qs + r * ld + c * E, x);
+      *reinterpret_cast<uint4*>(Qs + r * ld + c * E) = x;
     }
     float m[RM], l[RM], acc[RM][NC];
     int vis[RM];
@@ -108,11 +80,11 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
             kx = *reinterpret_cast<const uint4*>(kbase + at);
             vx = *reinterpret_cast<const uint4*>(vbase + at);
           } else {
-            raise_error(p.st, ERR_BAD_INDEX, 90);
+            raise_on_plan(p, pl, ERR_BAD_INDEX, 90);
           }
         }
-        put_words<T>(Ks + r * ld + c * E, kx);
-        put_words<T>(Vs + r * hd + c * E, vx);
+        *reinterpret_cast<uint4*>(Ks + r * ld + c * E) = kx;
+        *reinterpret_cast<uint4*>(Vs + r * hd + c * E) = vx;
       }
       __syncthreads();
       float s[RM][4] = {};
@@ -170,9 +142,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
       }
       __syncwarp();
     }
-    if (t0 > 0 || t1 < it.n_tiles) {
+    if (!walk.whole(it)) {
       // divided among CTAs: the last to arrive joins the parts
-      const int c0 = unit_cta(it.unit0, w.units, w.ctas), c1 = unit_cta(it.unit0 + it.n_tiles - 1, w.units, w.ctas);
+      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
       const int part_words = M * (hd + 2);
       float* mine = part_of(pl, part_words, cta, cta == c0);
 #pragma unroll
@@ -188,9 +160,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
       __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const int n = atomicAdd(&pl.arrived[w.item], 1);
+        const int n = atomicAdd(&pl.arrived[walk.index], 1);
         s_last = n == c1 - c0;
-        if (s_last) pl.arrived[w.item] = 0;
+        if (s_last) pl.arrived[walk.index] = 0;
       }
       __syncthreads();
       if (!s_last) continue;
@@ -219,10 +191,10 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
       const int r = ty * RM + i, j = r / G, h = it.kv_head * G + r % G;
       if (j >= it.n_rows) continue;
       const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : NAN);  // a row that sees no key gives zeros
-      T* dst = reinterpret_cast<T*>(a.o) + (int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * hd;
+      float* dst = reinterpret_cast<float*>(a.o) + (int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * hd;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (c < nc) dst[tx + 16 * c] = Conv<T>::out(acc[i][c] * inv);
+        if (c < nc) dst[tx + 16 * c] = acc[i][c] * inv;
       if (a.lse && tx == 0)
         a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m[i] == -INFINITY ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
     }
@@ -231,33 +203,25 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
 
 namespace {
 
-template <typename T, int M, int NC>
+template <int M, int NC>
 cudaError_t launch_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
   const size_t smem = 4 * (size_t)(M * (p.head_dim + 4) + kTile * (p.head_dim + 4) + kTile * p.head_dim + M * (kTile + 4));
-  cudaError_t e = cudaFuncSetAttribute(attention_simt_kernel<T, M, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+  cudaError_t e = cudaFuncSetAttribute(attention_simt_kernel<M, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_ex(attention_simt_kernel<T, M, NC>, dim3(pl.ctas), dim3(kThreads), smem, s, true, p, pl, a);
+  return launch_ex(attention_simt_kernel<M, NC>, dim3(pl.ctas), dim3(kThreads), smem, s, true, p, pl, a);
 }
 
-template <typename T, int M>
+template <int M>
 cudaError_t simt_dim(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
-  if (p.head_dim <= 64) return launch_simt<T, M, 4>(p, pl, a, s);
-  if (p.head_dim <= 128) return launch_simt<T, M, 8>(p, pl, a, s);
-  if constexpr (sizeof(T) == 4) return launch_simt<T, M, 16>(p, pl, a, s);
-  return cudaErrorInvalidValue;
+  if (p.head_dim <= 64) return launch_simt<M, 4>(p, pl, a, s);
+  if (p.head_dim <= 128) return launch_simt<M, 8>(p, pl, a, s);
+  return launch_simt<M, 16>(p, pl, a, s);
 }
 
 }  // namespace
 
-cudaError_t pages_attention_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, int dtype, bool few,
-                                 cudaStream_t s) {
-  auto run = [&](auto zero) {
-    using T = decltype(zero);
-    return few ? simt_dim<T, 16>(p, pl, a, s) : simt_dim<T, 64>(p, pl, a, s);
-  };
-  if (dtype == DUOLM_DTYPE_FP32) return run(0.f);
-  if (dtype == DUOLM_DTYPE_FP16) return run(__half{});
-  return run(__nv_bfloat16{});
+cudaError_t pages_attention_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool few, cudaStream_t s) {
+  return few ? simt_dim<16>(p, pl, a, s) : simt_dim<64>(p, pl, a, s);
 }
 
 }  // namespace duolm

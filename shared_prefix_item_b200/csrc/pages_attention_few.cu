@@ -1,0 +1,374 @@
+// Attention of a few query rows per sequence over a paged KV cache (16-bit
+// elements): up to 16 (token, query head) rows per KV head, so the work is
+// reading K and V once, and HBM bounds it.
+//
+// One pass with a running maximum, as in the other paths: S = Q K^T,
+// m' = max(m, max S), P = 2^(S - m'), l' = l 2^(m - m') + sum P,
+// O' = O 2^(m - m') + P V; S, m, l and O in fp32, P rounded to the cache's
+// type because it is a matrix operand.
+//
+// A tile is 64 keys.  One warp fetches tiles with TMA (a lane to each
+// 64-element box of a page, 128-byte swizzle), four warps each take 16 of the
+// tile's keys with statistics and O of their own, joined when the item ends:
+// no barrier between the four inside an item.  16 rows are half of the
+// smallest tcgen05 tile's quarter, and S and P would go through tensor memory
+// between two products of a few hundred cycles; mma.sync (m16n8k16) keeps them
+// in registers and needs a tenth of the time the tile's bytes take to arrive.
+// Two CTAs per SM, each with 96 KB of tiles in flight or in use, so that one
+// CTA's item ends are covered by the other's loads.
+#include "kernels.cuh"
+#include "pages.cuh"
+
+namespace duolm {
+
+namespace {
+
+constexpr int kTile = 64, kRows = 16;
+constexpr int kMathWarps = 4, kMath = 32 * kMathWarps, kThreads = kMath + 32;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int HD>
+struct Lay {
+  static constexpr int NH = HD / 64;               // 64-element halves of a row
+  static constexpr int HALF = kTile * 128;         // one half of a tile's K (or V)
+  static constexpr int STAGE = 2 * NH * HALF;      // K, then V
+  static constexpr int STAGES = 96 * 1024 / STAGE; // 3 (head_dim 128) or 6
+  static constexpr int LD = HD + 8;                // row of the joined O: 8 banks on per row
+  static constexpr int ACC = STAGES * STAGE, STAT = ACC + kRows * LD * 4, BAR = STAT + kMathWarps * kRows * 8;
+  static constexpr int SMEM = BAR + 16 * STAGES + 16 + 1024;
+};
+
+__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// c += a b, 16 x 8 x 16
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return BF16 ? pack_bf162(lo, hi) : pack_half2(lo, hi);
+}
+
+}  // namespace
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
+    pages_attention_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                               PagesView p, PagesPlan pl, AttnArgs a) {
+  using L = Lay<HD>;
+  constexpr int NH = L::NH, STAGES = L::STAGES, NT = HD / 8;  // NT: 8-column tiles of O
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + L::BAR;
+  auto full = [&](uint32_t s) { return bars + 16 * s; };
+  auto empty = [&](uint32_t s) { return bars + 16 * s + 8; };
+  int* s_last = reinterpret_cast<int*>(smem + L::BAR + 16 * STAGES);
+  float* acc = reinterpret_cast<float*>(smem + L::ACC);
+  float2* stat = reinterpret_cast<float2*>(smem + L::STAT);  // [warp][row] m, l
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kMathWarps && lane == 0) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kMathWarps);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  if (!plan_usable(p, pl)) return;
+  const int cta = blockIdx.x, G = a.group;
+  PageItem it;
+
+  if (warp == kMathWarps) {
+    // ---- TMA
+    const int box = min(p.page_tokens, kTile), boxes = kTile / box * NH;
+    const int bj = lane / NH, bh = lane % NH;
+    uint32_t n = 0;
+    bool ok = true;
+    for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
+      const int32_t* table = p.table + (int64_t)it.seq * p.max_pages;
+      auto fetch = [&](int t) {
+        const int key = t * kTile + bj * box;
+        return lane < boxes && key < it.n_keys ? table[key >> p.page_shift] : -1;
+      };
+      int id = fetch(walk.t0);
+      for (int t = walk.t0; t < walk.t1; ++t, ++n) {
+        const uint32_t slot = n % STAGES;
+        const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
+        const int left = it.n_keys - t * kTile;
+        const int n_boxes = left <= 0 ? 0 : min(kTile / box, (left + box - 1) / box) * NH;
+        const bool have = lane < n_boxes;
+        if (have && (unsigned)id >= (unsigned)p.n_pages) {
+          raise_on_plan(p, pl, ERR_BAD_INDEX, 120);
+          id = 0;
+        }
+        const int y = have ? ((id * p.n_kv_heads + it.kv_head) << p.page_shift) + ((t * kTile + bj * box) & (p.page_tokens - 1))
+                           : 0;
+        const uint32_t dst = sbase + slot * L::STAGE + bh * L::HALF + bj * box * 128;
+        if (!(ok = mbar_wait_warp(empty(slot), (n / STAGES & 1u) ^ 1u, p.st, 121))) break;
+        if (lane == 0) mbar_arrive_expect_tx(full(slot), 2 * n_boxes * box * 128);
+        __syncwarp();
+        if (have) {
+          tma_load_2d(&tmK, dst, full(slot), bh * 64, y);
+          tma_load_2d(&tmV, dst + NH * L::HALF, full(slot), bh * 64, y);
+        }
+        id = next_id;
+      }
+    }
+    // leave no copy in flight into shared memory that this CTA gives up
+    if (!ok)
+      for (uint32_t k = n > STAGES ? n - STAGES : 0; k < n; ++k) mbar_wait_warp(full(k % STAGES), k / STAGES & 1u, p.st, 122);
+    return;
+  }
+
+  // ---- math warps: keys [16 warp, 16 warp + 16) of every tile
+  const int g = lane >> 2, c2 = (lane & 3) * 2;
+  const float scale_log2 = a.scale * 1.4426950408889634f;
+  // lane's row of the four 8 x 8 matrices that one ldmatrix reads
+  const int k_key = warp * 16 + (lane >> 4) * 8 + (lane & 7), k_chunk = lane >> 3 & 1;
+  const int v_key = warp * 16 + (lane >> 3 & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
+  uint32_t n = 0;
+  bool ok = true;
+  for (ItemWalk walk(pl, cta); walk.next(&it);) {
+    const int rows = min(kRows, it.n_rows * G);
+    // Q as the products' first operand: rows g and g + 8, elements 16 k + c2.. and 16 k + 8 + c2..
+    uint32_t qf[HD / 16][4];
+    int vis[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i, j = r / G;
+      vis[i] = a.causal ? min(max(it.last0 + j + 1, 0), it.n_keys) : it.n_keys;
+      const char* src = a.q + ((int64_t)(it.row0 + j) * a.q_stride + (int64_t)(it.kv_head * G + r % G) * HD) * 2;
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          qf[k][i + 2 * h] = r < rows ? *reinterpret_cast<const uint32_t*>(src + (16 * k + 8 * h + c2) * 2) : 0u;
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int t = walk.t0; t < walk.t1; ++t, ++n) {
+      const uint32_t slot = n % STAGES;
+      ok = ok && mbar_wait_warp(full(slot), n / STAGES & 1u, p.st, 123);
+      if (!ok) continue;
+      const int k0 = t * kTile + warp * 16;
+      if (k0 < it.n_keys) {
+        const uint32_t kb = sbase + slot * L::STAGE + k_key * 128, vb = sbase + slot * L::STAGE + NH * L::HALF + v_key * 128;
+        float s[4][4] = {};  // two chains per 8 keys, so that the products do not wait on one another
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          uint32_t kf[4];
+          ldsm4(kf, kb + (k >> 2) * L::HALF + ((((k & 3) * 2 + k_chunk) ^ (k_key & 7)) << 4));
+          mma16<BF16>(s[(k & 1) * 2], qf[k], kf[0], kf[1]);
+          mma16<BF16>(s[(k & 1) * 2 + 1], qf[k], kf[2], kf[3]);
+        }
+        uint32_t pf[4];
+        float corr[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // rows g, g + 8
+          float x[4];
+          const int left = vis[i] - k0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] = s[j >> 1][2 * i + (j & 1)] + s[2 + (j >> 1)][2 * i + (j & 1)];
+            if (8 * (j >> 1) + c2 + (j & 1) >= left) x[j] = -INFINITY;
+          }
+          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float m_new = fmaxf(m[i], mx * scale_log2);
+          const float base = m_new == -INFINITY ? 0.f : m_new;  // no key of this row yet
+          corr[i] = fast_exp2(m[i] - base);
+          m[i] = m_new;
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[j] = fast_exp2(fmaf(x[j], scale_log2, -base));
+          l[i] = l[i] * corr[i] + ((e[0] + e[1]) + (e[2] + e[3]));  // of this lane's columns
+          pf[i] = pack2<BF16>(e[0], e[1]);
+          pf[2 + i] = pack2<BF16>(e[2], e[3]);
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+          for (int t2 = 0; t2 < NT; ++t2) {
+            o[t2][0] *= corr[0];
+            o[t2][1] *= corr[0];
+            o[t2][2] *= corr[1];
+            o[t2][3] *= corr[1];
+          }
+        }
+        // V rows behind the last key: the weights are 0 there, but the slots
+        // may hold anything, and 0 x NaN is NaN
+        const int tail = it.n_keys - k0;
+        const uint32_t lo = (c2 < tail ? 0xffffu : 0u) | (c2 + 1 < tail ? 0xffff0000u : 0u);
+        const uint32_t hi = (c2 + 8 < tail ? 0xffffu : 0u) | (c2 + 9 < tail ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c) {
+          uint32_t vf[4];
+          ldsm4_t(vf, vb + (c >> 2) * L::HALF + ((((c & 3) * 2 + v_chunk) ^ (v_key & 7)) << 4));
+          mma16<BF16>(o[2 * c], pf, vf[0] & lo, vf[1] & hi);
+          mma16<BF16>(o[2 * c + 1], pf, vf[2] & lo, vf[3] & hi);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(slot));
+    }
+    // ---- the item's end: the four warps' parts joined, one after the other
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if ((lane & 3) == 0) stat[warp * kRows + g + 8 * i] = make_float2(m[i], l[i]);
+    }
+    math_sync();
+    float wt[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kMathWarps; ++w) mm = fmaxf(mm, stat[w * kRows + g + 8 * i].x);
+      wt[i] = fast_exp2(m[i] - (mm == -INFINITY ? 0.f : mm));
+    }
+#pragma unroll 1
+    for (int w = 0; w < kMathWarps; ++w) {
+      if (w == warp)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (g + 8 * i < rows)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              float2* dst = reinterpret_cast<float2*>(acc + (g + 8 * i) * L::LD + t * 8 + c2);
+              float2 x = w ? *dst : make_float2(0.f, 0.f);
+              x.x = fmaf(o[t][2 * i], wt[i], x.x);
+              x.y = fmaf(o[t][2 * i + 1], wt[i], x.y);
+              *dst = x;
+            }
+      math_sync();
+    }
+    // out, four elements to a thread; or, divided among CTAs, a part, and the
+    // last CTA to arrive joins the parts in CTA order
+    const bool whole = walk.whole(it);
+    const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
+    constexpr int kPart = kRows * (HD + 2), W4 = HD / 4;
+    bool last = whole;
+    if (!whole) {
+      float* part = part_of(pl, kPart, cta, cta == c0);
+      for (int e = threadIdx.x; e < rows * W4; e += kMath) {
+        const int r = e / W4, c = e % W4;
+        __stcg(reinterpret_cast<float4*>(part) + e, *reinterpret_cast<const float4*>(acc + r * L::LD + 4 * c));
+      }
+      if (threadIdx.x < rows) {
+        float mm = -INFINITY, ll = 0.f;
+        for (int w = 0; w < kMathWarps; ++w) mm = fmaxf(mm, stat[w * kRows + threadIdx.x].x);
+        for (int w = 0; w < kMathWarps; ++w) {
+          const float2 s = stat[w * kRows + threadIdx.x];
+          ll += s.y * fast_exp2(s.x - (mm == -INFINITY ? 0.f : mm));
+        }
+        __stcg(reinterpret_cast<float2*>(part + kRows * HD) + threadIdx.x, make_float2(mm, ll));
+      }
+      __threadfence();
+      math_sync();
+      if (threadIdx.x == 0) {
+        const int k = atomicAdd(&pl.arrived[walk.index], 1);
+        *s_last = k == c1 - c0;
+        if (*s_last) pl.arrived[walk.index] = 0;
+      }
+      math_sync();
+      last = *s_last;
+      __threadfence();
+    }
+    if (last && ok) {
+      const int n_parts = whole ? kMathWarps : c1 - c0 + 1;
+      auto part = [&](int k) { return part_of(pl, kPart, c0 + k, k == 0); };
+      for (int e = threadIdx.x; e < rows * W4; e += kMath) {
+        const int r = e / W4, c = e % W4, j = r / G, h = it.kv_head * G + r % G;
+        auto stat_of = [&](int k) {
+          return whole ? stat[k * kRows + r] : __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * HD) + r);
+        };
+        float mm = -INFINITY, ll = 0.f;
+        for (int k = 0; k < n_parts; ++k) mm = fmaxf(mm, stat_of(k).x);
+        const float base = mm == -INFINITY ? 0.f : mm;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (whole) {
+          for (int k = 0; k < n_parts; ++k) ll += stat_of(k).y * fast_exp2(stat_of(k).x - base);
+          x = *reinterpret_cast<const float4*>(acc + r * L::LD + 4 * c);
+        } else {
+#pragma unroll 8
+          for (int k = 0; k < n_parts; ++k) {
+            const float2 s = stat_of(k);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(part(k)) + e);
+            const float w = fast_exp2(s.x - base);
+            ll = fmaf(s.y, w, ll);
+            x.x = fmaf(y.x, w, x.x);
+            x.y = fmaf(y.y, w, x.y);
+            x.z = fmaf(y.z, w, x.z);
+            x.w = fmaf(y.w, w, x.w);
+          }
+        }
+        const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // a row that sees no key gives zeros
+        *reinterpret_cast<uint2*>(a.o + ((int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD + 4 * c) * 2) =
+            make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
+        if (a.lse && c == 0)
+          a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = mm == -INFINITY ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      }
+    }
+    math_sync();  // acc and stat are read before the next item's
+  }
+  if (!ok && lane == 0) pl.head->stale = 1;
+}
+
+namespace {
+
+template <int HD, bool BF16>
+cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagesView& p, const PagesPlan& pl,
+                       const AttnArgs& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(pages_attention_few_kernel<HD, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Lay<HD>::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_ex(pages_attention_few_kernel<HD, BF16>, dim3(pl.ctas), dim3(kThreads), Lay<HD>::SMEM, s, true, tk, tv, p,
+                   pl, a);
+}
+
+}  // namespace
+
+cudaError_t pages_attention_few(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, cudaStream_t s) {
+  // (16-bit boxes are copied as they are, so bf16 uses the fp16 maps)
+  CUtensorMap tk, tv;
+  char err[128];
+  const uint64_t rows = (uint64_t)p.n_pages * p.n_kv_heads * p.page_tokens;
+  const uint32_t box = std::min(p.page_tokens, kTile);
+  const int64_t off = a.layer * p.layer_bytes();
+  if (!make_tmap_f16_2d(&tk, p.k + off, p.head_dim, rows, 64, box, err, sizeof err) ||
+      !make_tmap_f16_2d(&tv, p.v + off, p.head_dim, rows, 64, box, err, sizeof err))
+    return cudaErrorInvalidValue;
+  if (p.head_dim == 128) return bf16 ? launch_few<128, true>(tk, tv, p, pl, a, s) : launch_few<128, false>(tk, tv, p, pl, a, s);
+  return bf16 ? launch_few<64, true>(tk, tv, p, pl, a, s) : launch_few<64, false>(tk, tv, p, pl, a, s);
+}
+
+}  // namespace duolm

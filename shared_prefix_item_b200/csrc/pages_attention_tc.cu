@@ -1,0 +1,539 @@
+// Attention of a chunk of query rows over a paged KV cache on 5th-generation
+// tensor cores (16-bit elements).
+//
+// The softmax is one pass with a running maximum: for a tile of 128 keys
+// S = Q K^T, m' = max(m, max S), P = 2^(S - m'), l += sum P, O += P V, with O
+// (and l) rescaled by 2^(m - m') only when the maximum has grown by more than
+// 2^8; out = O / l.  S, O, m and l are fp32; P is rounded to the cache's type
+// because it is a tensor-core operand.
+//
+// An item (see the plan) is up to two sub-tiles of 128 (token, query head)
+// rows of one entry under one KV head, and a CTA has a range of its key
+// tiles.  Two softmax chains, A and B, keep the tensor core busy in turn:
+//   more than 128 rows: A and B are the two sub-tiles, and every K/V tile
+//     serves both;
+//   128 rows or fewer: both chains hold the same rows, A takes the even key
+//     tiles and B the odd ones, and A joins the two at the end (both O are in
+//     the same TMEM lanes, so no data but m and l crosses warps).
+// One CTA per SM, 384 threads:
+//   warps 0-3 softmax of A, 4-7 of B: a thread holds a row (its TMEM lane) and
+//             128 keys;
+//   warp 8    TMA: Q (one box of the entry's rows x the heads of the group),
+//             then K and V page by page, a lane to each box; 128-byte swizzle;
+//   warp 9    one lane issues tcgen05.mma, per tile first O_X += P_X V of the
+//             chain's previous tile (P read from tensor memory), then S_X;
+//   warp 10   V rows behind the last visible key are zeroed in shared memory
+//             before the tensor core reads them: P is 0 there, but the slots may
+//             hold anything, and 0 x NaN is NaN;
+//   warp 11   idle.
+// Tensor memory: S/P of A in columns [0, 128), of B in [128, 256), O of A from
+// 256, of B from 384.  tcgen05.mma of one thread run in issue order, so S_X may
+// be issued right behind the P V that reads the same columns, and its commit
+// reports both.  Every mbarrier wait is bounded; a warp whose wait gives up
+// raises the status and goes on through the remaining barriers without work.
+#include "kernels.cuh"
+#include "pages.cuh"
+
+namespace duolm {
+
+namespace {
+
+constexpr int kSub = 128, kKeys = 128;
+constexpr int kWG = 128, kThreads = 3 * kWG;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10;
+// registers move from the third warpgroup to the softmax (sum: the launch's 384 x 168)
+constexpr int kRegLaunch = 168, kRegSoftmax = 200, kRegOther = 104;
+static_assert(2 * kWG * kRegSoftmax + kWG * kRegOther <= kThreads * kRegLaunch, "register split above the launch's registers");
+constexpr int kHalf = 16384;  // 128 rows x 64 elements
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int HD>
+struct Lay {
+  static constexpr int NH = HD / 64;
+  static constexpr int SLOTS = HD == 64 ? 4 : 2;  // K and V tiles in flight: 64 KB each
+  static constexpr int Q = 0, K = Q + 2 * NH * kHalf, V = K + SLOTS * NH * kHalf, BAR = V + SLOTS * NH * kHalf;
+  static constexpr int STAT = BAR + 256;  // float2 [128]: m and l of chain B
+  static constexpr int SMEM = STAT + 1024 + 1024;
+};
+
+enum { B_QFULL, B_QEMPTY, B_SFULL0, B_SFULL1, B_PFULL0, B_PFULL1, B_OFULL0, B_OFULL1, B_DRAIN, B_KV };
+// then per slot: K full, K empty, V full, V empty, V raw (a tile whose rows are still to be zeroed)
+template <int HD>
+__device__ __forceinline__ int kv_bar(int kind, uint32_t slot) { return B_KV + kind * Lay<HD>::SLOTS + slot; }
+enum { KFULL, KEMPTY, VFULL, VEMPTY, VRAW };
+
+__device__ __forceinline__ void named_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(2 * kWG) : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return BF16 ? pack_bf162(lo, hi) : pack_half2(lo, hi);
+}
+
+}  // namespace
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    pages_attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                              const __grid_constant__ CUtensorMap tmV, PagesView p, PagesPlan pl, AttnArgs a) {
+  using L = Lay<HD>;
+  constexpr int NH = L::NH, SLOTS = L::SLOTS;
+  constexpr uint32_t kIdescS = BF16 ? idesc_bf16_f32(kSub, kKeys) : idesc_f16_f32(kSub, kKeys);
+  constexpr uint32_t kIdescPV = (BF16 ? idesc_bf16_f32(kSub, HD) : idesc_f16_f32(kSub, HD)) | (1u << 16);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  auto kvbar = [&](int kind, uint32_t slot) { return smem_u32(bars + kv_bar<HD>(kind, slot)); };
+  constexpr int kBars = B_KV + 5 * SLOTS;
+  static_assert(kBars * 8 + 8 <= 256, "barriers");
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kBars);
+  int* s_last = reinterpret_cast<int*>(tmem_holder + 1);
+  float2* stat = reinterpret_cast<float2*>(smem + L::STAT);
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.group, sub_tokens = kSub / G;
+  if (warp == kWarpTma && lane == 0) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), (i == B_PFULL0 || i == B_PFULL1) ? (uint32_t)kWG : 1u);
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  const bool usable = plan_usable(p, pl);
+  const int cta = blockIdx.x;
+  PageItem it;
+
+  // Every role walks the same items and tiles, so their running counts agree
+  // and give each barrier's phase.
+  if (!usable) {
+    // straight to the teardown
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
+    const int X = warp >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = tmem + lane_off + 128 * X, tO = tmem + lane_off + 256 + 128 * X;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    uint32_t n_xt = 0, n_xi = 0;
+    bool ok = true;
+    for (ItemWalk walk(pl, cta); walk.next(&it);) {
+      const bool two = it.n_rows > sub_tokens;  // two sub-tiles of rows
+      const int nt = walk.t1 - walk.t0;
+      const int j = r / G + (two ? X * sub_tokens : 0);
+      const bool valid = r < sub_tokens * G && j < it.n_rows;
+      const bool live = __any_sync(0xffffffffu, valid);
+      const int vis = a.causal ? min(max(it.last0 + j + 1, 0), it.n_keys) : it.n_keys;
+      float m_used = -INFINITY, l = 0.f;
+      const int step = two ? 1 : 2, first = two ? 0 : X;
+      for (int lt = first; lt < nt; lt += step, ++n_xt) {
+        ok = ok && mbar_wait_warp(bar(B_SFULL0 + X), n_xt & 1u, p.st, 100);
+        if (!ok || !live) {
+          mbar_arrive(bar(B_PFULL0 + X));
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, sr[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) tmem_ld_fence(sr[c][i]);
+        const int n_vis = vis - (walk.t0 + lt) * kKeys;  // of this tile
+        if (__any_sync(0xffffffffu, n_vis < kKeys)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= n_vis) sr[c][i] = __float_as_uint(-INFINITY);
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx[(i >> 1) & 3] = fmax3f(mx[(i >> 1) & 3], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+        const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2);
+        // decided for the whole warp, as the rescale is warp-collective, by its
+        // own rows alone: slots of no row hold what shared memory held
+        if (lt == first) {
+          m_used = m_new;
+        } else if (__any_sync(0xffffffffu, valid && m_new > m_used + kRescaleLog2)) {
+          const float corr = m_new == m_used ? 1.f : fast_exp2(m_used - m_new);
+#pragma unroll 1
+          for (int c = 0; c < HD / 32; ++c) {
+            float v[32];
+            tmem_ld32(tO + 32 * c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= corr;
+            tmem_st32(tO + 32 * c, v);
+          }
+          l *= corr;
+          m_used = m_new;
+        }
+        const float nmu = m_used == -INFINITY ? 0.f : -m_used;  // no key of this row yet
+        const float2 sv = make_float2(scale_log2, scale_log2), nv = make_float2(nmu, nmu);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = ffma2(make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])), sv, nv);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            ls[i & 1] = fadd2(ls[i & 1], e);
+            pk[i] = pack2<BF16>(e.x, e.y);
+          }
+          tmem_st16_async(tS + 16 * c, pk);
+        }
+        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(B_PFULL0 + X));
+      }
+      // ---- the item's end.  O_X is overwritten only by the P V of the next
+      // item's first P, which this warpgroup releases after reading it.
+      const bool mine = first < nt;  // this chain had tiles
+      if (mine) {
+        ok = ok && mbar_wait_warp(bar(B_OFULL0 + X), n_xi & 1u, p.st, 101);
+        ++n_xi;
+        tc_fence_after();
+      }
+      const bool joined = !two && nt > 1;  // A takes over B's half of the keys
+      const bool writes = two || X == 0;
+      float wa = 1.f, wb = 0.f;
+      if (joined) {
+        if (X == 1) stat[r] = make_float2(m_used, l);
+        named_sync(1);
+        if (X == 0) {
+          const float2 sb = stat[r];
+          const float m = fmaxf(m_used, sb.x), base = m == -INFINITY ? 0.f : m;
+          wa = fast_exp2(m_used - base);
+          wb = fast_exp2(sb.x - base);
+          l = l * wa + sb.y * wb;
+          m_used = m;
+        }
+      }
+      const bool whole = walk.whole(it);
+      const int h = it.kv_head * G + r % G;
+      const bool act = writes && live && ok;
+      float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a row that sees no key gives zeros
+      char* dst = a.o + ((int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD) * 2;
+      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
+      constexpr int kPart = 2 * kSub * (HD + 2), kRows = 2 * kSub;
+      const int slot = (two ? X * kSub : 0) + r;
+      float* part = part_of(pl, kPart, cta, cta == c0);
+      if (act) {
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32_async(tO + 32 * c, ov);
+          if (joined) {
+            uint32_t ob[32];
+            tmem_ld32_async(tO + 128 + 32 * c, ob);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              tmem_ld_fence(ov[i]);
+              tmem_ld_fence(ob[i]);
+              ov[i] = __float_as_uint(__uint_as_float(ov[i]) * wa + __uint_as_float(ob[i]) * wb);
+            }
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) tmem_ld_fence(ov[i]);
+          }
+          if (valid && whole) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                w[i] = pack2<BF16>(__uint_as_float(ov[16 * k + 2 * i]) * inv, __uint_as_float(ov[16 * k + 2 * i + 1]) * inv);
+              uint4* d4 = reinterpret_cast<uint4*>(dst + 64 * c + 32 * k);
+              d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              __stcg(reinterpret_cast<uint4*>(part) + (8 * c + i) * kRows + slot,
+                     make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]));
+          }
+        }
+        tc_fence_before();
+        if (valid && !whole) __stcg(reinterpret_cast<float2*>(part + kRows * HD) + slot, make_float2(m_used, l));
+        if (valid && whole && a.lse)
+          a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m_used == -INFINITY ? -INFINITY : (m_used + log2f(l)) * kLn2;
+      }
+      if (joined) named_sync(2);  // A has read O of B
+      if (whole) continue;
+      // ---- divided among CTAs: the last to arrive joins the parts, in CTA order
+      __threadfence();
+      named_sync(3);
+      if (threadIdx.x == 0) {
+        const int n = atomicAdd(&pl.arrived[walk.index], 1);
+        *s_last = n == c1 - c0;
+        if (*s_last) pl.arrived[walk.index] = 0;
+      }
+      named_sync(4);
+      if (!*s_last || !act || !valid) continue;
+      __threadfence();
+      float m = -INFINITY;
+      for (int c = c0; c <= c1; ++c)
+        m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(part_of(pl, kPart, c, c == c0) + kRows * HD) + slot).x);
+      const float base = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float2 s = __ldcg(reinterpret_cast<const float2*>(part_of(pl, kPart, c, c == c0) + kRows * HD) + slot);
+        l += s.y * fast_exp2(s.x - base);
+      }
+      inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+      for (int k = 0; k < HD / 16; ++k) {
+        float4 acc[4] = {};
+        for (int c = c0; c <= c1; ++c) {
+          const float* pc = part_of(pl, kPart, c, c == c0);
+          const float w = fast_exp2(__ldcg(reinterpret_cast<const float2*>(pc + kRows * HD) + slot).x - base);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pc) + (4 * k + i) * kRows + slot);
+            acc[i].x += w * v.x, acc[i].y += w * v.y, acc[i].z += w * v.z, acc[i].w += w * v.w;
+          }
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = pack2<BF16>(acc[i].x * inv, acc[i].y * inv);
+          w[2 * i + 1] = pack2<BF16>(acc[i].z * inv, acc[i].w * inv);
+        }
+        uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * k);
+        d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      if (a.lse)
+        a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    if (!ok && lane == 0) pl.head->stale = 1;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
+    if (warp == kWarpTma) {
+      // ---- TMA: a lane to each 64-element box of a page
+      const int box = min(p.page_tokens, kKeys), boxes = kKeys / box * NH;
+      const int bj = lane / NH, bh = lane % NH;
+      uint32_t n_kv = 0, n_it = 0, raw_par = 0, raw_last = 0;
+      bool ok = true;
+      for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
+        const int32_t* table = p.table + (int64_t)it.seq * p.max_pages;
+        auto fetch = [&](int t) {
+          const int key = t * kKeys + bj * box;
+          return lane < boxes && key < it.n_keys ? table[key >> p.page_shift] : -1;
+        };
+        const bool two = it.n_rows > sub_tokens;
+        int id = fetch(walk.t0);
+        ok = mbar_wait_warp(bar(B_QEMPTY), (n_it & 1u) ^ 1u, p.st, 102);
+        if (!ok) break;
+        if (lane == 0) {
+          const int subs = two ? 2 : 1;
+          mbar_arrive_expect_tx(bar(B_QFULL), subs * NH * sub_tokens * G * 128);
+          for (int s = 0; s < subs; ++s)
+            for (int h = 0; h < NH; ++h)
+              tma_load_3d(&tmQ, sbase + L::Q + (s * NH + h) * kHalf, bar(B_QFULL), h * 64, it.kv_head * G,
+                          it.row0 + s * sub_tokens);
+        }
+        ++n_it;
+        for (int t = walk.t0; t < walk.t1; ++t, ++n_kv) {
+          const uint32_t slot = n_kv % SLOTS, par = (n_kv / SLOTS & 1u) ^ 1u;
+          const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
+          const int left = it.n_keys - t * kKeys;  // keys of this tile
+          const int n_boxes = left <= 0 ? 0 : min(kKeys / box, (left + box - 1) / box) * NH;
+          const bool have = lane < n_boxes;
+          if (have && (unsigned)id >= (unsigned)p.n_pages) {
+            raise_on_plan(p, pl, ERR_BAD_INDEX, 103);
+            id = 0;
+          }
+          const int y = have ? ((id * p.n_kv_heads + it.kv_head) << p.page_shift) +
+                                   ((t * kKeys + bj * box) & (p.page_tokens - 1))
+                             : 0;
+          const uint32_t off = bh * kHalf + bj * box * 128;
+          if (!(ok = mbar_wait_warp(kvbar(KEMPTY, slot), par, p.st, 104))) break;
+          if (lane == 0) mbar_arrive_expect_tx(kvbar(KFULL, slot), n_boxes * box * 128);
+          __syncwarp();
+          if (have) tma_load_2d(&tmK, sbase + L::K + slot * NH * kHalf + off, kvbar(KFULL, slot), bh * 64, y);
+          raw_last &= ~(1u << slot);
+          if (!(ok = mbar_wait_warp(kvbar(VEMPTY, slot), par, p.st, 105))) {
+            ++n_kv;
+            raw_last |= 1u << (slot + 8);  // K armed, V not
+            break;
+          }
+          const bool tail = left < kKeys;
+          const uint32_t vb = kvbar(tail ? VRAW : VFULL, slot);
+          if (lane == 0) mbar_arrive_expect_tx(vb, n_boxes * box * 128);
+          __syncwarp();
+          if (have) tma_load_2d(&tmV, sbase + L::V + slot * NH * kHalf + off, vb, bh * 64, y);
+          if (tail) {
+            raw_last |= 1u << slot;
+            raw_par ^= 1u << slot;
+          }
+          id = next_id;
+        }
+      }
+      if (!ok && lane == 0) {
+        // leave no copy in flight into shared memory that this CTA gives up
+        if (n_it > 0) mbar_wait(bar(B_QFULL), (n_it - 1) & 1u, p.st, 106);
+        for (uint32_t k = n_kv > SLOTS ? n_kv - SLOTS : 0; k < n_kv; ++k) {
+          const uint32_t slot = k % SLOTS, par = k / SLOTS & 1u;
+          mbar_wait(kvbar(KFULL, slot), par, p.st, 106);
+          if (raw_last >> slot & 1u)
+            mbar_wait(kvbar(VRAW, slot), (raw_par >> slot & 1u) ^ 1u, p.st, 106);
+          else if (!(raw_last >> (slot + 8) & 1u))
+            mbar_wait(kvbar(VFULL, slot), par, p.st, 106);
+        }
+      }
+    } else if (warp == kWarpTail) {
+      uint32_t n_kv = 0, raw_par = 0;
+      bool ok = true;
+      for (ItemWalk walk(pl, cta); ok && walk.next(&it);)
+        for (int t = walk.t0; t < walk.t1 && ok; ++t, ++n_kv) {
+          const int left = max(0, it.n_keys - t * kKeys);
+          if (left >= kKeys) continue;
+          const uint32_t slot = n_kv % SLOTS;
+          if (!(ok = mbar_wait_warp(kvbar(VRAW, slot), raw_par >> slot & 1u, p.st, 107))) break;
+          raw_par ^= 1u << slot;
+          uint8_t* v = smem + L::V + slot * NH * kHalf;
+          for (int h = 0; h < NH; ++h)
+            for (int i = left * 8 + lane; i < kKeys * 8; i += 32)
+              *reinterpret_cast<uint4*>(v + h * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kvbar(VFULL, slot));
+        }
+    } else if (warp == kWarpMma && lane == 0) {
+      // ---- MMA issuer (state in named registers)
+      struct Pending {  // P V of a chain's tile, issued before its next S
+        int valid, first, last, release_v;
+        uint32_t slot, par, xt;
+      };
+      Pending pa{}, pb{};
+      uint32_t n_kv = 0, xt_a = 0, xt_b = 0, n_it = 0;
+      bool ok = true;
+      auto issue_pv = [&](int X, Pending& q) -> bool {
+        if (!mbar_wait(bar(B_PFULL0 + X), q.xt & 1u, p.st, 108)) return false;
+        if (!mbar_wait(kvbar(VFULL, q.slot), q.par, p.st, 109)) return false;
+        tc_fence_after();
+        const uint32_t tS = tmem + 128 * X, tO = tmem + 256 + 128 * X;
+        const uint32_t vbase = sbase + L::V + q.slot * NH * kHalf;
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          tc_mma_f16_ts(tO, tS + 8 * k, smem_desc_sw128_mn(vbase + k * 2048, kHalf), kIdescPV, (q.first && k == 0) ? 0u : 1u);
+        if (q.last) tc_commit(bar(B_OFULL0 + X));
+        if (q.release_v) tc_commit(kvbar(VEMPTY, q.slot));
+        q.valid = 0;
+        return true;
+      };
+      auto issue_s = [&](int X, int q_sub, uint32_t slot) {
+        const uint32_t qbase = sbase + L::Q + q_sub * NH * kHalf, kbase = sbase + L::K + slot * NH * kHalf;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          tc_mma_f16(tmem + 128 * X, smem_desc_sw128(qbase + (k >> 2) * kHalf + (k & 3) * 32),
+                     smem_desc_sw128(kbase + (k >> 2) * kHalf + (k & 3) * 32), kIdescS, k > 0 ? 1u : 0u);
+        tc_commit(bar(B_SFULL0 + X));
+      };
+      for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
+        const bool two = it.n_rows > sub_tokens;
+        const int nt = walk.t1 - walk.t0;
+        if (!(ok = mbar_wait(bar(B_QFULL), n_it & 1u, p.st, 110))) break;
+        ++n_it;
+        for (int lt = 0; lt < nt; ++lt, ++n_kv) {
+          const uint32_t slot = n_kv % SLOTS, par = n_kv / SLOTS & 1u;
+          if (!(ok = mbar_wait(kvbar(KFULL, slot), par, p.st, 111))) break;
+          if (two) {
+            if (pa.valid && !(ok = issue_pv(0, pa))) break;
+            tc_fence_after();
+            issue_s(0, 0, slot);
+            pa = Pending{1, lt == 0, lt == nt - 1, 0, slot, par, xt_a++};
+            if (pb.valid && !(ok = issue_pv(1, pb))) break;
+            tc_fence_after();
+            issue_s(1, 1, slot);
+            pb = Pending{1, lt == 0, lt == nt - 1, 1, slot, par, xt_b++};
+          } else if (lt & 1) {
+            if (pb.valid && !(ok = issue_pv(1, pb))) break;
+            tc_fence_after();
+            issue_s(1, 0, slot);
+            pb = Pending{1, lt == 1, lt >= nt - 2, 1, slot, par, xt_b++};
+          } else {
+            if (pa.valid && !(ok = issue_pv(0, pa))) break;
+            tc_fence_after();
+            issue_s(0, 0, slot);
+            pa = Pending{1, lt == 0, lt >= nt - 2, 1, slot, par, xt_a++};
+            // what the last item left of the other chain
+            if (lt == 0 && pb.valid && !(ok = issue_pv(1, pb))) break;
+          }
+          tc_commit(kvbar(KEMPTY, slot));
+          if (lt == nt - 1) tc_commit(bar(B_QEMPTY));
+        }
+      }
+      if (ok && pa.valid) ok = issue_pv(0, pa);
+      if (ok && pb.valid) ok = issue_pv(1, pb);
+      // no tensor-core operation of this CTA may outlive its TMEM
+      tc_commit(bar(B_DRAIN));
+      mbar_wait(bar(B_DRAIN), 0, p.st, 112);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+namespace {
+
+template <int HD, bool BF16>
+cudaError_t launch_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagesView& p,
+                      const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(pages_attention_tc_kernel<HD, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Lay<HD>::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_ex(pages_attention_tc_kernel<HD, BF16>, dim3(pl.ctas), dim3(kThreads), Lay<HD>::SMEM, s, true, tq, tk, tv,
+                   p, pl, a);
+}
+
+}  // namespace
+
+cudaError_t pages_attention_tc(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, int n_rows,
+                               cudaStream_t s) {
+  // (16-bit boxes are copied as they are, so bf16 uses the fp16 maps)
+  CUtensorMap tq, tk, tv;
+  char err[128];
+  const uint64_t hd = p.head_dim, rows = (uint64_t)p.n_pages * p.n_kv_heads * p.page_tokens;
+  const uint64_t qdims[3] = {hd, (uint64_t)a.n_q_heads, (uint64_t)n_rows};
+  const uint64_t qstr[2] = {hd * 2, (uint64_t)a.q_stride * 2};
+  const uint32_t qbox[3] = {64, (uint32_t)a.group, (uint32_t)(kSub / a.group)};
+  const uint32_t box = std::min(p.page_tokens, kKeys);
+  const int64_t off = a.layer * p.layer_bytes();
+  if (!make_tmap_f16_3d(&tq, a.q, qdims, qstr, qbox, err, sizeof err) ||
+      !make_tmap_f16_2d(&tk, p.k + off, hd, rows, 64, box, err, sizeof err) ||
+      !make_tmap_f16_2d(&tv, p.v + off, hd, rows, 64, box, err, sizeof err))
+    return cudaErrorInvalidValue;
+  if (p.head_dim == 128)
+    return bf16 ? launch_tc<128, true>(tq, tk, tv, p, pl, a, s) : launch_tc<128, false>(tq, tk, tv, p, pl, a, s);
+  return bf16 ? launch_tc<64, true>(tq, tk, tv, p, pl, a, s) : launch_tc<64, false>(tq, tk, tv, p, pl, a, s);
+}
+
+}  // namespace duolm

@@ -5,20 +5,25 @@
 namespace duolm {
 
 PagesPath pages_path(int dtype, int64_t max_rows, int group) {
-  return max_rows * group <= 16 ? kPathSimt16 : kPathSimt64;
+  const bool few = std::max<int64_t>(max_rows, 1) * group <= 16;
+  if (dtype == DUOLM_DTYPE_FP32) return few ? kPathSimt16 : kPathSimt64;
+  return few ? kPathFew : kPathTc;
 }
 
 PathShape pages_path_shape(PagesPath path, int head_dim) {
   PathShape sh{};
-  sh.slots = path == kPathSimt16 ? 16 : 64;
-  sh.keys = 64;
-  sh.part_words = sh.slots * (head_dim + 2);
+  sh.slots = path == kPathSimt64 ? 64 : path == kPathTc ? 128 : 16;
+  sh.subs = path == kPathTc ? 2 : 1;
+  sh.keys = path == kPathTc ? 128 : 64;
+  sh.grain = path == kPathTc ? 4 : 8;
+  sh.ctas_per_sm = path == kPathFew ? 2 : 1;
+  sh.part_words = sh.subs * sh.slots * (head_dim + 2);
   return sh;
 }
 
 int64_t pages_plan_layout(char* base, int64_t n, int64_t n_rows, int n_kv_heads, int group, PathShape sh, int ctas,
                           PagesPlan* out) {
-  const int64_t tokens = sh.slots / group;  // of one item
+  const int64_t tokens = sh.tokens(group);
   const int64_t max_items = n_kv_heads * (n + n_rows / tokens);
   if (max_items >= kScanCap) return -1;
   int64_t at = 0;
@@ -72,19 +77,21 @@ __device__ __forceinline__ bool entry_of(const PagesView& p, const BatchView& b,
   return true;
 }
 
-// key tiles of the query rows [r0, r0 + m) of an entry (one at least: an item
-// that sees no key still writes its rows)
+// keys that the query rows [r0, r0 + m) of an entry see
 __device__ __forceinline__ int item_keys(const BatchView& b, int rows, int len, int r0, int m) {
   return b.causal ? max(0, len - rows + min(r0 + m, rows)) : len;
 }
 
+__device__ __forceinline__ int key_tiles(int n_keys, int keys) { return max(1, (n_keys + keys - 1) / keys); }  // one at least: an item that sees no key still writes its rows
+
 // CTA 0: the attention's items and how the CTAs divide their key tiles.  The
 // other CTAs: where each query row's token lies in the cache.
 __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, BatchView b, PagesPlan pl, int m,
-                                                                  int keys) {
+                                                                  int keys, int grain) {
   extern __shared__ uint32_t seen[];
   __shared__ int s_scan[32];
   __shared__ uint32_t s_err;
+  __shared__ unsigned long long s_tiles;
   pdl_launch_dependents();
   if (blockIdx.x > 0) {
     pdl_wait();
@@ -118,10 +125,26 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
     return;
   }
   for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
-  if (threadIdx.x == 0) s_err = 0;
+  if (threadIdx.x == 0) s_err = 0, s_tiles = 0;
   __syncthreads();
   pdl_wait();
-  if (pages_raised(p)) return;
+  if (pages_raised(p)) {
+    if (threadIdx.x == 0) pl.head->stale = 1;
+    return;
+  }
+  // A batch of few tiles is divided in units of several: a CTA then takes
+  // longer over them, but fewer items are divided and joined.
+  for (int i = threadIdx.x; i < b.n; i += kPlanThreads) {
+    int s, o, rows, len;
+    uint32_t err = 0;
+    if (!entry_of(p, b, i, &s, &o, &rows, &len, &err)) continue;
+    unsigned long long u = 0;
+    for (int t = 0; t < rows; t += m) u += key_tiles(item_keys(b, rows, len, t, m), keys);
+    atomicAdd(&s_tiles, u * p.n_kv_heads);
+  }
+  __syncthreads();
+  if (s_tiles > (unsigned long long)pl.ctas * grain) grain = 1;
+  const int unit_keys = keys * grain;
   int items = 0, units = 0;
   for (int i0 = 0; i0 < b.n; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
@@ -137,7 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
       } else {
         const int tiles = (rows + m - 1) / m;
         int64_t u = 0;
-        for (int t = 0; t < tiles; ++t) u += max(1, (item_keys(b, rows, len, t * m, m) + keys - 1) / keys);
+        for (int t = 0; t < tiles; ++t) u += key_tiles(item_keys(b, rows, len, t * m, m), unit_keys);
         n_it = tiles * p.n_kv_heads;
         n_un = (int)min(u * p.n_kv_heads, (int64_t)kScanCap);
       }
@@ -152,8 +175,8 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   if (s_err || units >= kScanCap || items > pl.max_items) {
     if (threadIdx.x == 0) {
       raise_error(p.st, s_err ? s_err : (uint32_t)ERR_BAD_LENGTH, 86);
-      pl.head->n_items = 0;
-      pl.head->units = pl.head->ctas = 0;
+      pl.head->n_items = pl.head->units = pl.head->ctas = 0;
+      pl.head->stale = 1;
     }
     return;
   }
@@ -162,6 +185,9 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
     pl.head->n_items = items;
     pl.head->units = units;
     pl.head->ctas = ctas;
+    pl.head->stale = 0;
+    pl.head->key = pl.key;
+    pl.head->grain = grain;
   }
   for (int i = threadIdx.x; i < items; i += kPlanThreads) pl.arrived[i] = 0;
   const int lane = threadIdx.x & 31;
@@ -174,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
     int per_head = 0;  // units of one head's items
     for (int t0 = 0; t0 < tiles; t0 += 32) {
       const int t = t0 + lane;
-      int u = t < tiles ? max(1, (item_keys(b, rows, len, t * m, m) + keys - 1) / keys) : 0;
+      int u = t < tiles ? key_tiles(item_keys(b, rows, len, t * m, m), unit_keys) : 0;
 #pragma unroll
       for (int o2 = 16; o2 > 0; o2 >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o2);
       per_head += u;
@@ -183,7 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
     for (int t0 = 0; t0 < tiles; t0 += 32) {
       const int t = t0 + lane;
       const int nk = t < tiles ? item_keys(b, rows, len, t * m, m) : 0;
-      const int u = t < tiles ? max(1, (nk + keys - 1) / keys) : 0;
+      const int u = t < tiles ? key_tiles(nk, unit_keys) : 0;
       int x = u;
 #pragma unroll
       for (int o2 = 1; o2 < 32; o2 <<= 1) {
@@ -200,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
           it.last0 = b.causal ? len - rows + t * m : 0;
           it.n_keys = nk;
           it.unit0 = base.y + h * per_head + before + x - u;
-          it.n_tiles = u;
+          it.n_tiles = key_tiles(nk, keys);
           const int k = base.x + h * tiles + t;
           pl.items[k] = it;
           // CTAs whose first unit is in this item
@@ -258,7 +284,7 @@ __global__ void __launch_bounds__(256) pages_write_kernel(PagesView p, PagesPlan
   constexpr int HPW = 32 / SEG;       // heads a warp holds at a time
   pdl_launch_dependents();
   pdl_wait();
-  if (pages_raised(p)) return;
+  if (!plan_usable(p, pl)) return;
   const int lane = threadIdx.x & 31, seg = lane / SEG, sl = lane % SEG;
   const int half = p.head_dim / 2;
   const bool in = sl * E < half;  // head_dim / 2 below SEG words: idle lanes
@@ -391,9 +417,17 @@ int batch_layout(const duolm_pages* pages, const PagesView& p, const duolm_pages
   if (!*sms) return pages_fail(DUOLM_E_CUDA, "device %d", pages->device);
   const int group = b->n_q_heads / p.n_kv_heads;
   *path = pages_path(pages->dtype, b->max_rows, group);
+  const PathShape sh = pages_path_shape(*path, p.head_dim);
   const int64_t need = pages_plan_layout(static_cast<char*>(b->plan), b->n, b->n_rows, p.n_kv_heads, group,
-                                         pages_path_shape(*path, p.head_dim), *sms, pl);
+                                         sh, *sms * sh.ctas_per_sm, pl);
   if (need < 0) return pages_fail(DUOLM_E_CAPACITY, "batch: too many items");
+  // FNV-1a of every size that an index in the plan goes by
+  uint32_t key = 2166136261u;
+  for (int64_t x : {(int64_t)b->n, (int64_t)b->n_rows, (int64_t)b->n_q_heads, (int64_t)(b->causal != 0), (int64_t)*path,
+                    (int64_t)*sms, (int64_t)p.n_kv_heads, (int64_t)p.head_dim, (int64_t)p.page_tokens, (int64_t)p.n_pages,
+                    (int64_t)p.n_seqs, (int64_t)p.max_pages})
+    for (int i = 0; i < 8; ++i) key = (key ^ (uint32_t)(x >> (8 * i) & 255)) * 16777619u;
+  pl->key = key;
   if (b->plan_bytes < need)
     return pages_fail(DUOLM_E_CAPACITY, "plan of %lld bytes, %lld needed", (long long)b->plan_bytes, (long long)need);
   return 0;
@@ -416,9 +450,8 @@ extern "C" int64_t duolm_pages_plan_bytes(const duolm_pages* pages, int n, int n
   const int sms = pages_sms(pages->device);
   if (!sms) return pages_fail(DUOLM_E_CUDA, "pages_plan_bytes: device %d", pages->device);
   const int group = n_q_heads / p.n_kv_heads;
-  const int64_t need = pages_plan_layout(nullptr, n, n_rows, p.n_kv_heads, group,
-                                         pages_path_shape(pages_path(pages->dtype, max_rows, group), p.head_dim), sms,
-                                         nullptr);
+  const PathShape sh = pages_path_shape(pages_path(pages->dtype, max_rows, group), p.head_dim);
+  const int64_t need = pages_plan_layout(nullptr, n, n_rows, p.n_kv_heads, group, sh, sms * sh.ctas_per_sm, nullptr);
   return need < 0 ? pages_fail(DUOLM_E_CAPACITY, "pages_plan_bytes: too many items") : need;
 }
 
@@ -442,7 +475,7 @@ extern "C" int duolm_pages_plan(const duolm_pages* pages, const duolm_pages_batc
     e = cudaFuncSetAttribute(batch_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
   if (e == cudaSuccess)
     e = launch_ex(batch_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(cuda_stream), true,
-                  p, b, pl, sh.slots / group, sh.keys);
+                  p, b, pl, sh.tokens(group), sh.keys, sh.grain);
   return e == cudaSuccess ? 0 : pages_fail(DUOLM_E_CUDA, "pages_plan: %s", cudaGetErrorString(e));
 }
 
@@ -518,6 +551,14 @@ extern "C" int duolm_pages_attention(const duolm_pages* pages, const duolm_pages
   if (!g.ok()) return pages_fail(DUOLM_E_CUDA, "pages_attention: device %d", pages->device);
   const AttnArgs a{static_cast<const char*>(q), static_cast<char*>(out), lse, q_stride, out_stride, batch->n_q_heads,
                    batch->n_q_heads / p.n_kv_heads, batch->causal != 0, layer, scale};
-  const cudaError_t e = pages_attention_simt(p, pl, a, pages->dtype, path == kPathSimt16, static_cast<cudaStream_t>(cuda_stream));
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const bool bf16 = pages->dtype == DUOLM_DTYPE_BF16;
+  cudaError_t e;
+  if (path == kPathFew)
+    e = pages_attention_few(p, pl, a, bf16, s);
+  else if (path == kPathTc)
+    e = pages_attention_tc(p, pl, a, bf16, batch->n_rows, s);
+  else
+    e = pages_attention_simt(p, pl, a, path == kPathSimt16, s);
   return e == cudaSuccess ? 0 : pages_fail(DUOLM_E_CUDA, "pages_attention: %s", cudaGetErrorString(e));
 }

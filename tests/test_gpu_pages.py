@@ -273,6 +273,7 @@ def test_a_refused_fork_changes_nothing(src, dst, tokens):
 @pytest.mark.parametrize("seqs, off", [([0, 0], [0, 1, 2]), ([0, 8], [0, 1, 2]), ([0, 3], [0, 2, 1]), ([0, 3], [1, 2, 3]),
                                        ([0, 3], [0, 1, 9])])
 def test_a_refused_plan_runs_nothing(seqs, off):
+    import shared_prefix_item_b200 as S
     torch = _t()
     c = Cache(n_pages=16, n_seqs=8, max_pages=16)
     c.resize([0, 3], [20, 1])
@@ -286,9 +287,16 @@ def test_a_refused_plan_runs_nothing(seqs, off):
         bad.plan()
         bad.attention(0, q, out, None, 0.125)
     _refused(c, -1, call)
-    bad.attention(0, q, out, None, 0.125)  # the plan of the refused call holds no work
-    c.c.check()
+    for _ in range(2):  # its plan is refused until the batch is planned again
+        bad.attention(0, q, out, None, 0.125)
+        with pytest.raises(S.DuolmError) as e:
+            c.c.check()
+        assert e.value.code == -8
     assert bool((out == 5.0).all())
+    b.plan()
+    b.attention(0, q, out, None, 0.125)
+    c.c.check()
+    assert not bool((out == 5.0).any())
 
 
 def test_page_ids_out_of_range_are_reported_not_followed():
@@ -311,6 +319,7 @@ def test_page_ids_out_of_range_are_reported_not_followed():
                 c.c.check()
             assert e.value.code == -7
             c.table[0, 2] = was
+            b.plan()
         b.attention(0, q, out, None, 0.125)
         c.c.check()
 
