@@ -388,21 +388,29 @@ class Ranker:
 # copied.  ``stream`` is a cudaStream_t handle (None: the default stream).
 
 _PAGE_DTYPES = {"torch.float32": DTYPE_FP32, "torch.bfloat16": DTYPE_BF16, "torch.float16": DTYPE_FP16}
+_names: dict = {}  # a dtype's name (naming one takes longer than all other checks of an argument)
+
+
+def _dtype_name(t) -> str:
+    d = t.dtype
+    n = _names.get(d)
+    if n is None:
+        n = _names[d] = str(d)
+    return n
 
 
 def _on(t, name: str, device: int):
-    d = t.device
-    if d.type != "cuda" or d.index != device:
-        raise ValueError(f"{name} is on {d}, the cache on cuda:{device}")
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}")
     return t
 
 
 def _ints(t, name: str, device: int, shape=None) -> int:
     """Pointer of a contiguous int32 device array of this shape (None: any 1-D)."""
     _on(t, name, device)
-    if str(t.dtype) != "torch.int32" or not t.is_contiguous():
+    if _dtype_name(t) != "torch.int32" or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 array is wanted")
-    if (t.dim() != 1) if shape is None else (tuple(t.shape) != tuple(shape)):
+    if (t.dim() != 1) if shape is None else (t.shape != shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, {'one dimension' if shape is None else tuple(shape)} wanted")
     return t.data_ptr()
 
@@ -445,6 +453,7 @@ class PagedCache:
         self._ref = ctypes.byref(self.desc)
         self.device, self.dtype = dev, k.dtype
         self.n_kv_heads, self.head_dim = H, D
+        self._table_shape, self._refs_shape = (S, M), (N,)
 
     @staticmethod
     def workspace_bytes(n_pages: int, n_seqs: int) -> int:
@@ -469,9 +478,8 @@ class PagedCache:
     def compact(self, table_out, refs_out, live_out, stream: Optional[int] = None):
         """Live pages move to the lowest ids; the tables that go with them are
         written to the outputs (which may be the cache's own)."""
-        d = self.desc
-        _pages_rc(lib.duolm_pages_compact(self._ref, _ints(table_out, "table_out", self.device, (d.n_seqs, d.max_pages)),
-                                          _ints(refs_out, "refs_out", self.device, (d.n_pages,)),
+        _pages_rc(lib.duolm_pages_compact(self._ref, _ints(table_out, "table_out", self.device, self._table_shape),
+                                          _ints(refs_out, "refs_out", self.device, self._refs_shape),
                                           _ints(live_out, "live_out", self.device, (1,)), stream))
 
     def check(self, stream: Optional[int] = None):
@@ -498,7 +506,7 @@ class PagedBatch:
         self.desc = PagesBatch(n, int(n_rows), int(max_rows), int(n_q_heads), 1 if causal else 0, 0,
                                _ints(seq, "seq", dev), _ints(offset, "offset", dev, (n + 1,)), plan.data_ptr(),
                                _bytes(plan, "plan", dev))
-        self.cache = cache
+        self.cache, self.n_rows, self.n_q_heads = cache, int(n_rows), int(n_q_heads)
         self._arrays = (seq, offset, plan)
         self._ref = ctypes.byref(self.desc)
 
@@ -508,18 +516,21 @@ class PagedBatch:
         _on(t, name, c.device)
         if t.dtype != c.dtype:
             raise ValueError(f"{name} of {t.dtype}, the cache of {c.dtype}")
-        want, st = (self.desc.n_rows, heads, c.head_dim), t.stride()
-        flat = t.dim() == 2 and tuple(t.shape) == (want[0], heads * c.head_dim) and st[1] == 1
-        if not flat and not (tuple(t.shape) == want and st[2] == 1 and (heads == 1 or st[1] == c.head_dim)):
-            raise ValueError(f"{name}: shape {tuple(t.shape)} strides {st}, rows of {heads} x {c.head_dim} contiguous "
-                             f"elements ({want[0]} of them) are wanted")
-        return t.data_ptr(), (st[0] if want[0] > 1 else heads * c.head_dim)
+        n, hd, st = self.n_rows, c.head_dim, t.stride()
+        if t.dim() == 3:
+            good = t.shape == (n, heads, hd) and st[2] == 1 and (heads == 1 or st[1] == hd)
+        else:
+            good = t.shape == (n, heads * hd) and st[1] == 1
+        if not good:
+            raise ValueError(f"{name}: shape {tuple(t.shape)} strides {st}, rows of {heads} x {hd} contiguous "
+                             f"elements ({n} of them) are wanted")
+        return t.data_ptr(), (st[0] if n > 1 else heads * hd)
 
     def _floats(self, t, name: str, shape) -> Optional[int]:
         if t is None:
             return None
         _on(t, name, self.cache.device)
-        if str(t.dtype) != "torch.float32" or not t.is_contiguous() or (shape and tuple(t.shape) != shape):
+        if _dtype_name(t) != "torch.float32" or not t.is_contiguous() or (shape and t.shape != shape):
             raise ValueError(f"{name}: contiguous float32 {shape or ''} is wanted, got {t.dtype} {tuple(t.shape)}")
         return t.data_ptr()
 
@@ -534,8 +545,8 @@ class PagedBatch:
         c, hd = self.cache, self.cache.head_dim
         kp, ks = self._rows(k, "k", c.n_kv_heads)
         vp, vs = self._rows(v, "v", c.n_kv_heads)
-        qp, qs = self._rows(q, "q", self.desc.n_q_heads) if q is not None else (None, 0)
-        op, os_ = self._rows(q_out, "q_out", self.desc.n_q_heads) if q is not None else (None, 0)
+        qp, qs = self._rows(q, "q", self.n_q_heads) if q is not None else (None, 0)
+        op, os_ = self._rows(q_out, "q_out", self.n_q_heads) if q is not None else (None, 0)
         if rope is not None and (rope.dim() != 3 or tuple(rope.shape[1:]) != (hd // 2, 2)):
             raise ValueError(f"rope: [positions, {hd // 2}, 2] is wanted, got {tuple(rope.shape)}")
         _pages_rc(lib.duolm_pages_write(c._ref, self._ref, int(layer), qp, qs, kp, ks, vp, vs,
@@ -546,11 +557,11 @@ class PagedBatch:
     def attention(self, layer: int, q, out, lse, scale: float, stream: Optional[int] = None):
         """Attention of the batch's rows over their sequences' pages; lse
         (None, or float32 [n_rows, n_q_heads]) the log of the softmax's sum."""
-        c, h = self.cache, self.desc.n_q_heads
+        c, h = self.cache, self.n_q_heads
         qp, qs = self._rows(q, "q", h)
         op, os_ = self._rows(out, "out", h)
         _pages_rc(lib.duolm_pages_attention(c._ref, self._ref, int(layer), qp, qs, float(scale), op, os_,
-                                            self._floats(lse, "lse", (self.desc.n_rows, h)), stream))
+                                            self._floats(lse, "lse", (self.n_rows, h)), stream))
 
 
 def _pages_rc(rc: int) -> int:

@@ -1,11 +1,12 @@
 // Paged KV cache: forking, growing, freeing and compacting sequences.
 //
-// Two kernels to a call.  One CTA decides: it checks every entry before
-// anything changes (a refused call changes nothing), ranks the free pages and
-// writes what is to be done to the workspace.  Then a whole grid does it:
-// tables and counts, a warp per sequence, and the page copies, a warp per
-// (page, layer, K or V, head).  The split keeps the decision, which needs a
-// prefix sum over all entries, out of the copies, which need every SM.
+// One kernel to a call, in two steps.  The first CTA to start decides: it
+// checks every entry before anything changes (a refused call changes nothing),
+// ranks the free pages and writes what is to be done to the workspace.  The
+// others wait for its word, and then the whole grid does it: tables and
+// counts, a warp per sequence, and the page copies.  The decision needs a
+// prefix sum over all entries, the copies need every SM; a second launch
+// between them cost 2 us of the host's time and 1.5 us of the GPU's.
 #include "pages.cuh"
 
 #include <cstdarg>
@@ -76,43 +77,220 @@ int pages_view(const duolm_pages* p, PagesView* out) {
 
 namespace {
 
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+
+// ---------------------------------------------------------------------------
+// The decision.  A call of little work runs as one cluster of up to kCluster
+// CTAs, whose first CTA decides while the others wait at the cluster's barrier.
+// A larger grid uses the status' last two words (0 between calls): turns taken
+// (low half) and CTAs done (high half), and the decider's word.  Whoever takes
+// turn 0 runs already and waits for nobody, so the others' wait ends whatever
+// order the CTAs start in.  Only the decider looks at the error flags: a CTA
+// that started late must not take an error of this call for an earlier one's.
+// ---------------------------------------------------------------------------
+constexpr int kCluster = 8;
+enum : uint32_t { kWordNone = 0, kWordGo = 1, kWordStop = 2 };
+
+template <typename Decide>
+__device__ __forceinline__ bool decided(const PagesView& p, Decide decide) {
+  __shared__ uint32_t s_word;
+  if (gridDim.x <= kCluster) {
+    if (blockIdx.x == 0) {
+      const bool go = !pages_raised(p) && decide();
+      __syncthreads();
+      if (threadIdx.x == 0) s_word = go ? kWordGo : kWordStop;
+      if (gridDim.x == 1) {
+        __syncthreads();
+        return s_word == kWordGo;
+      }
+      __threadfence();
+    }
+    cluster_sync();
+    uint32_t word = 0;
+    if (threadIdx.x == 0) {
+      word = ld_shared_cluster_u32(map_to_rank(smem_u32(&s_word), 0));
+    }
+    word = __syncthreads_or(word == kWordGo);
+    cluster_sync();  // the decider's shared memory is read while it lives
+    return word;
+  }
+  if (threadIdx.x == 0) s_word = atomicAdd(&p.st->pad[0], 1u) & 0xffffu;
+  __syncthreads();
+  if (s_word == 0) {
+    const bool go = !pages_raised(p) && decide();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s_word = go ? kWordGo : kWordStop;
+      __threadfence();
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&p.st->pad[1]), "r"(s_word) : "memory");
+    }
+  } else {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t w = kWordNone;
+      uint64_t t0 = 0;
+      for (uint32_t i = 1; !w; ++i) {
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(w) : "l"(&p.st->pad[1]) : "memory");
+        if (!w && (i & 255u) == 0) {
+          const uint64_t now = global_ns();
+          if (!t0) t0 = now;
+          if (now - t0 > kWaitLimitNs) {
+            raise_error(p.st, ERR_WAIT_TIMEOUT, 79);
+            w = kWordStop;
+          }
+        }
+      }
+      s_word = w;
+    }
+  }
+  __syncthreads();
+  return s_word == kWordGo;
+}
+// Every CTA's last step: the last one puts the words back.
+__device__ __forceinline__ void done(const PagesView& p) {
+  if (gridDim.x <= kCluster) return;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  __threadfence();
+  if (atomicAdd(&p.st->pad[0], 0x10000u) >> 16 == gridDim.x - 1) {
+    p.st->pad[1] = kWordNone;
+    p.st->pad[0] = 0;
+  }
+}
+
+// what the decider wrote, past the L1
+__device__ __forceinline__ PageCopy copy_of(const PagesWork& w, int64_t i) {
+  const int4 x = __ldcg(reinterpret_cast<const int4*>(w.copies) + i);
+  return PageCopy{x.x, x.y, x.z, x.w};
+}
+
+// ---------------------------------------------------------------------------
+// Page copies: rows [0, rows) of every (layer, K or V, head) of the listed
+// pages, by bulk copies through shared memory: one lane of each warp keeps
+// kDepth loads of 4 KB in flight, and the stores behind them, over a ring of
+// its own, so 16 warps have 128 KB on the way to every SM and no thread touches
+// the data.  HBM bound (read + write).  Pieces of 2 KB (ring of 6, 3 in flight)
+// measured 76.6 against 73.6 us for 256 forks through 28 layers, 1 KB 90.6,
+// 8 warps with rings of 6 x 4 KB 97.9; whole pages (compaction) 173 us in all.
+// ---------------------------------------------------------------------------
+constexpr int kPiece = 4096, kRing = 3, kDepth = 2;
+constexpr int kRingBytes = kWarps * kRing * kPiece;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// ring: the CTA's dynamic shared memory, with no generic access to it behind
+// the last __syncthreads(); bars: [kWarps * kRing], initialised
+__device__ __forceinline__ void copy_pages(const PagesView& p, const PagesWork& w, int n, uint32_t ring, uint32_t bars) {
+  if ((threadIdx.x & 31) != 0 || n == 0) return;
+  const int warp_in = threadIdx.x >> 5;
+  ring += warp_in * kRing * kPiece;
+  bars += warp_in * kRing * 8;
+  const int per_page = 2 * p.n_layers * p.n_kv_heads, row_bytes = p.head_dim * p.elem;
+  const int64_t units = (int64_t)n * per_page, step = (int64_t)gridDim.x * kWarps;
+  int64_t u = (int64_t)warp_in * gridDim.x + blockIdx.x;  // the first units spread over the SMs
+  if (u >= units) return;
+  PageCopy next = copy_of(w, u / per_page);
+  const char* src = nullptr;  // of the unit's rest
+  char* dst = nullptr;
+  int left = 0;
+  // the pieces whose loads are on the way
+  char* to[kDepth];
+  int bytes[kDepth];
+  bool ok = true, more = true;
+  uint32_t i = 0;
+  for (; ok; ++i) {
+    while (more && left == 0) {
+      if (u >= units) {
+        more = false;
+        break;
+      }
+      const int r = (int)(u % per_page), h = r % p.n_kv_heads, lv = r / p.n_kv_heads;
+      const PageCopy pc = next;
+      char* base = (lv & 1 ? p.v : p.k) + (lv >> 1) * p.layer_bytes() + h * p.head_bytes();
+      src = base + pc.src * p.page_bytes();
+      dst = base + pc.dst * p.page_bytes();
+      left = pc.rows * row_bytes;
+      u += step;
+      if (u < units) next = copy_of(w, u / per_page);
+    }
+    const int was = bytes[kDepth - 1];
+    char* was_to = to[kDepth - 1];
+#pragma unroll
+    for (int k = kDepth - 1; k > 0; --k) bytes[k] = bytes[k - 1], to[k] = to[k - 1];
+    bytes[0] = 0;
+    if (more) {
+      // the store that last read this slot is kRing pieces back, with
+      // kRing - 1 - kDepth stores behind it
+      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kRing - 1 - kDepth) : "memory");
+      const uint32_t slot = i % kRing, b = min(left, kPiece);
+      mbar_arrive_expect_tx(bars + 8 * slot, b);
+      bulk_load(ring + slot * kPiece, src, b, bars + 8 * slot);
+      bytes[0] = b;
+      to[0] = dst;
+      src += b;
+      dst += b;
+      left -= b;
+    }
+    if (i < kDepth) {
+      if (!more && i == 0) break;
+      continue;
+    }
+    if (was == 0) break;  // nothing was loaded kDepth pieces ago, nor since
+    const uint32_t j = i - kDepth;
+    if (!(ok = mbar_wait(bars + 8 * (j % kRing), j / kRing & 1u, p.st, 78))) break;
+    bulk_store(was_to, ring + j % kRing * kPiece, was);
+  }
+  if (!ok)  // no copy may be in flight into shared memory that this CTA gives up
+    for (int k = 0; k <= kDepth; ++k)
+      if (k == kDepth || bytes[k]) mbar_wait(bars + 8 * ((i - k) % kRing), (i - k) / kRing & 1u, p.st, 78);
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ void init_bars(uint64_t* bars) {
+  if (threadIdx.x >= kWarps * kRing) return;
+  mbar_init(smem_u32(bars + threadIdx.x), 1);
+  fence_barrier_init();
+}
+
 // ---------------------------------------------------------------------------
 // resize: entry i gets the pages for length[i] tokens, gives back what lies
 // behind them, and, where it grows out of a partly filled page that others
 // hold too, a copy of that page.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesView p, PagesWork w, int n,
-                                                                   const int32_t* __restrict__ seq,
-                                                                   const int32_t* __restrict__ length) {
-  extern __shared__ uint32_t seen[];
-  __shared__ int s_scan[32];
-  __shared__ uint32_t s_err;
-  pdl_launch_dependents();
-  for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
-  if (threadIdx.x == 0) s_err = 0;
+__device__ __forceinline__ bool resize_decide(const PagesView& p, const PagesWork& w, int n, const int32_t* __restrict__ seq,
+                                              const int32_t* __restrict__ length, uint32_t* seen, int* s_scan,
+                                              uint32_t* s_err) {
+  for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kThreads) seen[i] = 0;
+  if (threadIdx.x == 0) *s_err = 0;
   __syncthreads();
-  pdl_wait();
-  if (pages_raised(p)) return;
   int64_t need_all = 0;
   int copies = 0;
-  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
     int need = 0, cow = 0, have = 0, want = 0;
     if (i < n) {
       const int s = seq[i], len = length ? length[i] : 0;
       if ((unsigned)s >= (unsigned)p.n_seqs || !claim(seen, s)) {
-        atomicOr(&s_err, ERR_BAD_SEQ);
+        atomicOr(s_err, ERR_BAD_SEQ);
       } else {
         const int old = p.length[s];
         if (len < 0 || len > p.max_tokens() || old < 0 || old > p.max_tokens()) {
-          atomicOr(&s_err, ERR_BAD_LENGTH);
+          atomicOr(s_err, ERR_BAD_LENGTH);
         } else {
           have = p.pages_of(old);
           want = p.pages_of(len);
           if (len > old && (old & (p.page_tokens - 1))) {
             const int tail = p.table[(int64_t)s * p.max_pages + have - 1];
             if ((unsigned)tail >= (unsigned)p.n_pages)
-              atomicOr(&s_err, ERR_BAD_INDEX);
+              atomicOr(s_err, ERR_BAD_INDEX);
             else
               cow = p.refs[tail] > 1;
           }
@@ -120,10 +298,13 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesView p, 
         }
       }
     }
-    int all, all_cow;
-    const int at = block_scan(need, s_scan, &all);
-    block_scan(cow, s_scan, &all_cow);
-    if (need_all + all > p.n_pages) atomicOr(&s_err, ERR_NO_PAGES);
+    // where nothing grows there is nothing to rank
+    int all = 0, all_cow = 0, at = 0;
+    if (__syncthreads_or(need)) {
+      at = block_scan<kThreads>(need, s_scan, &all);
+      block_scan<kThreads>(cow, s_scan, &all_cow);
+    }
+    if (need_all + all > p.n_pages) atomicOr(s_err, ERR_NO_PAGES);
     if (i < n) w.entry[i] = make_int4((int)(need_all + at), have, want, cow);
     need_all += all;
     copies += all_cow;
@@ -131,14 +312,14 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesView p, 
   __syncthreads();
   // the lowest free pages, in order, until there are enough
   int64_t found = 0;
-  for (int64_t b = 0; !s_err && found < need_all && b < p.n_pages; b += 4 * kPlanThreads) {
+  for (int64_t b = 0; !*s_err && found < need_all && b < p.n_pages; b += 4 * kThreads) {
     const int64_t id = b + 4 * threadIdx.x;
     int free4 = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (id + j < p.n_pages && p.refs[id + j] == 0) free4 |= 1 << j;
     int all;
-    int64_t at = found + block_scan(__popc(free4), s_scan, &all);
+    int64_t at = found + block_scan<kThreads>(__popc(free4), s_scan, &all);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (free4 >> j & 1) {
@@ -147,154 +328,129 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesView p, 
       }
     found += all;
   }
-  if (found < need_all && !s_err) {
-    if (threadIdx.x == 0) raise_error(p.st, ERR_NO_PAGES, 80);
-    return;
-  }
-  if (s_err) {
-    if (threadIdx.x == 0) raise_error(p.st, s_err, 81);
-    return;
+  const uint32_t err = *s_err | (found < need_all ? (uint32_t)ERR_NO_PAGES : 0u);
+  if (err) {
+    if (threadIdx.x == 0) raise_error(p.st, *s_err ? *s_err : err, 80);
+    return false;
   }
   if (threadIdx.x == 0) w.head[0] = copies;
-  if (!copies) return;
+  if (!copies) return true;
   __syncthreads();
   // the copies, in entry order
-  int done = 0;
-  for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+  int listed = 0;
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
     const int4 e = i < n ? w.entry[i] : make_int4(0, 0, 0, 0);
     int all;
-    const int at = done + block_scan(e.w, s_scan, &all);
+    const int at = listed + block_scan<kThreads>(e.w, s_scan, &all);
     if (e.w) {
       const int s = seq[i];
       w.copies[at] = PageCopy{p.table[(int64_t)s * p.max_pages + e.y - 1], w.list[e.x],
                               p.length[s] & (p.page_tokens - 1), 0};
     }
-    done += all;
+    listed += all;
   }
+  return true;
 }
 
-// Rows [0, rows) of every (layer, K or V, head) of the listed pages, a warp to
-// each: 16-byte words, eight in flight per lane.  HBM bound (read + write).
-__device__ __forceinline__ void copy_pages(const PagesView& p, const PageCopy* __restrict__ copies, int n, int warp,
-                                           int n_warps) {
-  const int lane = threadIdx.x & 31;
-  const int per_page = 2 * p.n_layers * p.n_kv_heads;
-  const int64_t head_words = p.head_bytes() / 16, page_words = p.page_bytes() / 16, layer_words = p.layer_bytes() / 16;
-  const int row_words = p.head_dim * p.elem / 16;
-  for (int64_t u = warp; u < (int64_t)n * per_page; u += n_warps) {
-    const int c = (int)(u / per_page), r = (int)(u % per_page);
-    const int h = r % p.n_kv_heads, lv = r / p.n_kv_heads;
-    const PageCopy pc = copies[c];
-    char* pool = lv & 1 ? p.v : p.k;
-    const int64_t base = (int64_t)(lv >> 1) * layer_words + h * head_words;
-    const uint4* src = reinterpret_cast<const uint4*>(pool) + base + pc.src * page_words;
-    uint4* dst = reinterpret_cast<uint4*>(pool) + base + pc.dst * page_words;
-    const int words = pc.rows * row_words;
-    for (int i = lane; i < words; i += 8 * 32) {
-      uint4 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + 32 * j < words) v[j] = __ldcg(src + i + 32 * j);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + 32 * j < words) dst[i + 32 * j] = v[j];
-    }
-  }
-}
-
-__global__ void __launch_bounds__(256) resize_apply_kernel(PagesView p, PagesWork w, int n,
-                                                           const int32_t* __restrict__ seq,
-                                                           const int32_t* __restrict__ length) {
+__global__ void __launch_bounds__(kThreads) resize_kernel(PagesView p, PagesWork w, int n, const int32_t* __restrict__ seq,
+                                                          const int32_t* __restrict__ length, bool may_copy) {
+  extern __shared__ __align__(128) uint8_t smem[];  // the decider's bitmap, then the copies' ring
+  __shared__ int s_scan[32];
+  __shared__ uint32_t s_err;
+  __shared__ uint64_t bars[kWarps * kRing];
   pdl_launch_dependents();
+  if (may_copy) init_bars(bars);
   pdl_wait();
-  if (pages_raised(p)) return;
-  const int lane = threadIdx.x & 31;
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, n_warps = (gridDim.x * blockDim.x) >> 5;
-  for (int i = warp; i < n; i += n_warps) {
-    const int s = seq[i];
-    const int4 e = w.entry[i];
-    int32_t* row = p.table + (int64_t)s * p.max_pages;
-    int next = e.x;
-    if (e.w) {  // the tail first: its copy is the entry's first page
-      if (lane == 0) {
-        const int fresh = w.list[next];
-        atomicSub(&p.refs[row[e.y - 1]], 1);
-        row[e.y - 1] = fresh;
+  const bool go = decided(p, [&] { return resize_decide(p, w, n, seq, length, reinterpret_cast<uint32_t*>(smem), s_scan, &s_err); });
+  if (go) {
+    const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    for (int i = warp; i < n; i += gridDim.x * kWarps) {
+      const int s = seq[i];
+      const int4 e = __ldcg(w.entry + i);
+      int32_t* row = p.table + (int64_t)s * p.max_pages;
+      int next = e.x;
+      if (e.w) {  // the tail first: its copy is the entry's first page
+        if (lane == 0) {
+          const int fresh = __ldcg(w.list + next);
+          atomicSub(&p.refs[row[e.y - 1]], 1);
+          row[e.y - 1] = fresh;
+          p.refs[fresh] = 1;
+        }
+        ++next;
+      }
+      for (int j = e.y + lane; j < e.z; j += 32) {
+        const int fresh = __ldcg(w.list + next + j - e.y);
+        row[j] = fresh;
         p.refs[fresh] = 1;
       }
-      ++next;
+      for (int j = e.z + lane; j < e.y; j += 32) {
+        const int gone = row[j];
+        if ((unsigned)gone < (unsigned)p.n_pages)
+          atomicSub(&p.refs[gone], 1);
+        else
+          raise_error(p.st, ERR_BAD_INDEX, 82);
+        row[j] = -1;
+      }
+      if (lane == 0) p.length[s] = length ? length[i] : 0;
     }
-    for (int j = e.y + lane; j < e.z; j += 32) {
-      const int fresh = w.list[next + j - e.y];
-      row[j] = fresh;
-      p.refs[fresh] = 1;
+    if (may_copy) {
+      fence_async_shared();  // the decider's bitmap lay where the copies go
+      __syncthreads();
+      copy_pages(p, w, __ldcg(w.head), smem_u32(smem), smem_u32(bars));
     }
-    for (int j = e.z + lane; j < e.y; j += 32) {
-      const int gone = row[j];
-      if ((unsigned)gone < (unsigned)p.n_pages)
-        atomicSub(&p.refs[gone], 1);
-      else
-        raise_error(p.st, ERR_BAD_INDEX, 82);
-      row[j] = -1;
-    }
-    if (lane == 0) p.length[s] = length ? length[i] : 0;
   }
-  copy_pages(p, w.copies, w.head[0], warp, n_warps);
+  done(p);
 }
 
 // ---------------------------------------------------------------------------
 // fork: dst starts as the first tokens[i] tokens of src, sharing its pages.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kPlanThreads) fork_check_kernel(PagesView p, int n, const int32_t* __restrict__ src,
-                                                                  const int32_t* __restrict__ dst,
-                                                                  const int32_t* __restrict__ tokens) {
+__global__ void __launch_bounds__(kThreads) fork_kernel(PagesView p, int n, const int32_t* __restrict__ src,
+                                                        const int32_t* __restrict__ dst,
+                                                        const int32_t* __restrict__ tokens) {
   extern __shared__ uint32_t seen[];
   __shared__ uint32_t s_err;
   pdl_launch_dependents();
-  for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
-  if (threadIdx.x == 0) s_err = 0;
-  __syncthreads();
   pdl_wait();
-  if (pages_raised(p)) return;
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-    const int d = dst[i];
-    if ((unsigned)d >= (unsigned)p.n_seqs || !claim(seen, d) || p.length[d] != 0) atomicOr(&s_err, ERR_BAD_SEQ);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-    const int s = src[i], t = tokens[i];
-    if ((unsigned)s >= (unsigned)p.n_seqs || (seen[s >> 5] >> (s & 31) & 1u))
-      atomicOr(&s_err, ERR_BAD_SEQ);
-    else if (t < 0 || t > p.length[s] || t > p.max_tokens())
-      atomicOr(&s_err, ERR_BAD_LENGTH);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0 && s_err) raise_error(p.st, s_err, 83);
-}
-
-__global__ void __launch_bounds__(256) fork_apply_kernel(PagesView p, int n, const int32_t* __restrict__ src,
-                                                         const int32_t* __restrict__ dst,
-                                                         const int32_t* __restrict__ tokens) {
-  pdl_launch_dependents();
-  pdl_wait();
-  if (pages_raised(p)) return;
-  const int lane = threadIdx.x & 31;
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, n_warps = (gridDim.x * blockDim.x) >> 5;
-  for (int i = warp; i < n; i += n_warps) {
-    const int t = tokens[i];
-    const int32_t* from = p.table + (int64_t)src[i] * p.max_pages;
-    int32_t* to = p.table + (int64_t)dst[i] * p.max_pages;
-    for (int j = lane; j < p.pages_of(t); j += 32) {
-      const int page = from[j];
-      to[j] = page;
-      if ((unsigned)page < (unsigned)p.n_pages)
-        atomicAdd(&p.refs[page], 1);
-      else
-        raise_error(p.st, ERR_BAD_INDEX, 84);
+  const bool go = decided(p, [&] {
+    for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kThreads) seen[i] = 0;
+    if (threadIdx.x == 0) s_err = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int d = dst[i];
+      if ((unsigned)d >= (unsigned)p.n_seqs || !claim(seen, d) || p.length[d] != 0) atomicOr(&s_err, ERR_BAD_SEQ);
     }
-    if (lane == 0) p.length[dst[i]] = t;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int s = src[i], t = tokens[i];
+      if ((unsigned)s >= (unsigned)p.n_seqs || (seen[s >> 5] >> (s & 31) & 1u))
+        atomicOr(&s_err, ERR_BAD_SEQ);
+      else if (t < 0 || t > p.length[s] || t > p.max_tokens())
+        atomicOr(&s_err, ERR_BAD_LENGTH);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && s_err) raise_error(p.st, s_err, 83);
+    return s_err == 0;
+  });
+  if (go) {
+    const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    for (int i = warp; i < n; i += gridDim.x * kWarps) {
+      const int t = tokens[i];
+      const int32_t* from = p.table + (int64_t)src[i] * p.max_pages;
+      int32_t* to = p.table + (int64_t)dst[i] * p.max_pages;
+      for (int j = lane; j < p.pages_of(t); j += 32) {
+        const int page = from[j];
+        to[j] = page;
+        if ((unsigned)page < (unsigned)p.n_pages)
+          atomicAdd(&p.refs[page], 1);
+        else
+          raise_error(p.st, ERR_BAD_INDEX, 84);
+      }
+      if (lane == 0) p.length[dst[i]] = t;
+    }
   }
+  done(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -302,27 +458,23 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(PagesView p, int n, con
 // k-th free page below n.  No page is both read and written, so the moves run
 // in any order, and the old copies stay as they were.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesView p, PagesWork w, int32_t* live_out) {
-  __shared__ int s_scan[32];
-  pdl_launch_dependents();
-  pdl_wait();
-  if (pages_raised(p)) return;
+__device__ __forceinline__ void compact_decide(const PagesView& p, const PagesWork& w, int32_t* live_out, int* s_scan) {
   int mine = 0, live;
-  for (int64_t id = threadIdx.x; id < p.n_pages; id += kPlanThreads) mine += p.refs[id] > 0;
-  block_scan(mine, s_scan, &live);
+  for (int64_t id = threadIdx.x; id < p.n_pages; id += kThreads) mine += p.refs[id] > 0;
+  block_scan<kThreads>(mine, s_scan, &live);
   int holes = 0, moved = 0;
-  for (int64_t b = 0; b < p.n_pages; b += kPlanThreads) {
+  for (int64_t b = 0; b < p.n_pages; b += kThreads) {
     const int64_t id = b + threadIdx.x;
     const int r = id < p.n_pages ? p.refs[id] : 0;
     const bool hole = id < live && r <= 0, mover = id >= live && id < p.n_pages && r > 0;
     int all;
     if (b < live) {
-      const int at = block_scan(hole, s_scan, &all);
+      const int at = block_scan<kThreads>(hole, s_scan, &all);
       if (hole) w.copies[holes + at].dst = (int)id;
       holes += all;
     }
-    if (b + kPlanThreads > live) {
-      const int at = block_scan(mover, s_scan, &all);
+    if (b + kThreads > live) {
+      const int at = block_scan<kThreads>(mover, s_scan, &all);
       if (mover) {
         PageCopy& c = w.copies[moved + at];
         c.src = (int)id;
@@ -334,7 +486,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesView p,
     if (id < p.n_pages && !mover) w.map[id] = id < live && r > 0 ? (int)id : -1;
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < moved; k += kPlanThreads) w.map[w.copies[k].src] = w.copies[k].dst;
+  for (int k = threadIdx.x; k < moved; k += kThreads) w.map[w.copies[k].src] = w.copies[k].dst;
   if (threadIdx.x == 0) {
     w.head[0] = moved;
     w.head[1] = live;
@@ -342,42 +494,65 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesView p,
   }
 }
 
-__global__ void __launch_bounds__(256) compact_apply_kernel(PagesView p, PagesWork w, int32_t* table_out,
-                                                            int32_t* refs_out) {
+__global__ void __launch_bounds__(kThreads) compact_kernel(PagesView p, PagesWork w, int32_t* table_out, int32_t* refs_out,
+                                                           int32_t* live_out) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_scan[32];
+  __shared__ uint64_t bars[kWarps * kRing];
   pdl_launch_dependents();
+  init_bars(bars);
   pdl_wait();
-  if (pages_raised(p)) return;
-  const int n = w.head[0], live = w.head[1];
-  const int64_t thread = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, threads = gridDim.x * (int64_t)blockDim.x;
-  for (int64_t i = thread; i < (int64_t)p.n_seqs * p.max_pages; i += threads) {
-    const int s = (int)(i / p.max_pages), j = (int)(i % p.max_pages);
-    int to = -1;
-    if (j < p.pages_of(p.length[s])) {
-      const int from = p.table[i];
-      to = (unsigned)from < (unsigned)p.n_pages ? w.map[from] : -1;
-      if (to < 0) raise_error(p.st, ERR_BAD_INDEX, 85);
+  const bool go = decided(p, [&] {
+    compact_decide(p, w, live_out, s_scan);
+    return true;
+  });
+  if (go) {
+    const int n = __ldcg(w.head), live = __ldcg(w.head + 1);
+    const int64_t thread = blockIdx.x * (int64_t)kThreads + threadIdx.x, threads = gridDim.x * (int64_t)kThreads;
+    for (int64_t i = thread; i < (int64_t)p.n_seqs * p.max_pages; i += threads) {
+      const int s = (int)(i / p.max_pages), j = (int)(i % p.max_pages);
+      int to = -1;
+      if (j < p.pages_of(p.length[s])) {
+        const int from = p.table[i];
+        to = (unsigned)from < (unsigned)p.n_pages ? __ldcg(w.map + from) : -1;
+        if (to < 0) raise_error(p.st, ERR_BAD_INDEX, 85);
+      }
+      table_out[i] = to;
     }
-    table_out[i] = to;
+    // counts: a page that stays keeps its own, a filled hole takes its page's
+    // (written below, from the list, so that refs_out may be refs itself)
+    for (int64_t id = thread; id < p.n_pages; id += threads) {
+      if (id >= live)
+        refs_out[id] = 0;
+      else if (__ldcg(w.map + id) >= 0)
+        refs_out[id] = p.refs[id];
+    }
+    for (int64_t k = thread; k < n; k += threads) {
+      const PageCopy c = copy_of(w, k);
+      refs_out[c.dst] = c.refs;
+    }
+    copy_pages(p, w, n, smem_u32(smem), smem_u32(bars));
   }
-  // counts: a page that stays keeps its own, a filled hole takes its page's
-  // (written below, from the list, so that refs_out may be refs itself)
-  for (int64_t id = thread; id < p.n_pages; id += threads) {
-    if (id >= live)
-      refs_out[id] = 0;
-    else if (w.map[id] >= 0)
-      refs_out[id] = p.refs[id];
-  }
-  for (int64_t k = thread; k < n; k += threads) refs_out[w.copies[k].dst] = w.copies[k].refs;
-  copy_pages(p, w.copies, n, (int)(thread >> 5), (int)(threads >> 5));
+  done(p);
 }
 
 size_t seen_bytes(const PagesView& p) { return (size_t)((p.n_seqs + 31) / 32) * 4; }
 
-// the bitmap of the largest cache (2^20 sequences) is 128 KB
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
-  return bytes <= 48 * 1024 - 512
-             ? cudaSuccess
-             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+// The kernels' shared memory is raised once per device, to the ring or to the
+// bitmap of the largest cache (2^20 sequences: 128 KB), whichever is larger.
+constexpr int kMaxSmem = kRingBytes > 128 * 1024 ? kRingBytes : 128 * 1024;
+cudaError_t allow_smem(int device) {
+  static std::mutex mu;
+  static bool raised[64] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (raised[device]) return cudaSuccess;
+  for (const void* f : {reinterpret_cast<const void*>(resize_kernel), reinterpret_cast<const void*>(fork_kernel),
+                        reinterpret_cast<const void*>(compact_kernel)}) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  raised[device] = true;
+  return cudaSuccess;
 }
 
 int launched(cudaError_t e, const char* what) {
@@ -388,6 +563,29 @@ int check_entries(const PagesView& v, int n, const char* what) {
   if (n < 0) return pages_fail(DUOLM_E_ARG, "%s: n = %d", what, n);
   if (n > v.n_seqs) return pages_fail(DUOLM_E_ARG, "%s: %d entries for %d sequences (one each)", what, n, v.n_seqs);
   return 0;
+}
+
+// A kernel for `warps` warps of work: one CTA, one cluster, or up to one CTA
+// per SM.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_for(int64_t warps, int sms, size_t smem, cudaStream_t s, void (*kernel)(KArgs...), Args&&... args) {
+  const int64_t ctas = (warps + kWarps - 1) / kWarps;
+  // (up to four units of work to a warp: a few 4 KB pieces take less than the
+  // turns and the word of a larger grid, about 3 us)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas <= 1 ? 1 : ctas <= 4 * kCluster ? kCluster : (unsigned)std::min<int64_t>(ctas, sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cfg.gridDim.x == kCluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 }  // namespace
@@ -415,11 +613,13 @@ extern "C" int duolm_pages_resize(const duolm_pages* pages, int n, const int32_t
   if (!g.ok() || !sms) return pages_fail(DUOLM_E_CUDA, "pages_resize: device %d", pages->device);
   const PagesWork w = pages_work(pages->workspace, p.n_pages, p.n_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(resize_plan_kernel), seen_bytes(p));
+  // only a growing sequence can leave a shared page: freeing needs no copies
+  const bool may_copy = length != nullptr;
+  const size_t smem = std::max<size_t>(seen_bytes(p), may_copy ? kRingBytes : 0);
+  cudaError_t e = allow_smem(pages->device);
   if (e == cudaSuccess)
-    e = launch_ex(resize_plan_kernel, dim3(1), dim3(kPlanThreads), seen_bytes(p), s, true, p, w, n, seq, length);
-  if (e == cudaSuccess)
-    e = launch_ex(resize_apply_kernel, dim3(4 * sms), dim3(256), 0, s, true, p, w, n, seq, length);
+    e = launch_for(may_copy ? 2ll * n * p.n_layers * p.n_kv_heads : n, sms, smem, s, resize_kernel, p, w, n, seq, length,
+                   may_copy);
   return launched(e, "pages_resize");
 }
 
@@ -434,12 +634,9 @@ extern "C" int duolm_pages_fork(const duolm_pages* pages, int n, const int32_t* 
   const int sms = pages_sms(pages->device);
   if (!g.ok() || !sms) return pages_fail(DUOLM_E_CUDA, "pages_fork: device %d", pages->device);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fork_check_kernel), seen_bytes(p));
+  cudaError_t e = allow_smem(pages->device);
   if (e == cudaSuccess)
-    e = launch_ex(fork_check_kernel, dim3(1), dim3(kPlanThreads), seen_bytes(p), s, true, p, n, src, dst, tokens);
-  if (e == cudaSuccess)
-    e = launch_ex(fork_apply_kernel, dim3(std::min((n + 7) / 8, 4 * sms)), dim3(256), 0, s, true, p, n, src, dst,
-                  tokens);
+    e = launch_for(n, sms, seen_bytes(p), s, fork_kernel, p, n, src, dst, tokens);
   return launched(e, "pages_fork");
 }
 
@@ -453,9 +650,12 @@ extern "C" int duolm_pages_compact(const duolm_pages* pages, int32_t* table_out,
   if (!g.ok() || !sms) return pages_fail(DUOLM_E_CUDA, "pages_compact: device %d", pages->device);
   const PagesWork w = pages_work(pages->workspace, p.n_pages, p.n_seqs);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e = launch_ex(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, true, p, w, live_out);
+  // at most half of the pages move; the tables' words, 32 to a warp
+  const int64_t warps = std::max<int64_t>((int64_t)p.n_pages * p.n_layers * p.n_kv_heads,
+                                          std::max<int64_t>((int64_t)p.n_seqs * p.max_pages, p.n_pages) / 32);
+  cudaError_t e = allow_smem(pages->device);
   if (e == cudaSuccess)
-    e = launch_ex(compact_apply_kernel, dim3(4 * sms), dim3(256), 0, s, true, p, w, table_out, refs_out);
+    e = launch_for(warps, sms, kRingBytes, s, compact_kernel, p, w, table_out, refs_out, live_out);
   return launched(e, "pages_compact");
 }
 

@@ -49,12 +49,12 @@ __device__ __forceinline__ bool pages_raised(const PagesView& p) {
 }
 
 // ---- one CTA deciding for a whole call ----------------------------------------
+// Exclusive prefix sum over the block's NT values of 0..kScanCap; *total:
+// their sum, where that is below kScanCap, else kScanCap (callers refuse it).
+// Uses s[32]; ends with the block in step.
 constexpr int kPlanThreads = 1024;
-
-// Exclusive prefix sum over the block's kPlanThreads values of 0..kScanCap;
-// *total: their sum, where that is below kScanCap, else kScanCap (callers
-// refuse it).  Uses s[32]; ends with the block in step.
 constexpr int kScanCap = 1 << 29;
+template <int NT = kPlanThreads>
 __device__ __forceinline__ int block_scan(int v, int* s, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -66,7 +66,7 @@ __device__ __forceinline__ int block_scan(int v, int* s, int* total) {
   if (lane == 31) s[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int y = s[lane];
+    int y = lane < NT / 32 ? s[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int z = __shfl_up_sync(0xffffffffu, y, o);
@@ -158,7 +158,8 @@ struct PlanHead {
 };
 struct PagesPlan {
   PlanHead* head;
-  int32_t* cta_item;  // [ctas] item holding the CTA's first unit
+  PageItem* cta_first;  // [ctas] item holding the CTA's first unit: which one, and the item itself
+  int32_t* cta_item;
   int32_t* arrived;   // [max_items] finished parts of a divided item (0 between calls)
   PageItem* items;    // [max_items]
   int2* base;         // [n + 1] per entry: items and units before it
@@ -188,11 +189,10 @@ struct CtaWork {  // a CTA's units [unit, end), the first of them in item `item`
   int unit, end, item, units, ctas, grain;
 };
 __device__ __forceinline__ CtaWork cta_work(const PagesPlan& pl, int cta) {
-  CtaWork w{0, 0, 0, pl.head->units, pl.head->ctas, pl.head->grain};
-  if (pl.head->n_items == 0 || cta >= w.ctas) return w;
+  CtaWork w{0, 0, pl.cta_item[cta], pl.head->units, pl.head->ctas, pl.head->grain};
+  if (cta >= w.ctas) return w;
   w.unit = cta_unit(cta, w.units, w.ctas);
   w.end = cta_unit(cta + 1, w.units, w.ctas);
-  w.item = pl.cta_item[cta];
   return w;
 }
 // A CTA's items in order, the next one's record already on its way.  Every
@@ -203,9 +203,8 @@ struct ItemWalk {
   PageItem next_item;
   int index;   // of the item next() gave last
   int t0, t1;  // its key tiles that are this CTA's
-  __device__ ItemWalk(const PagesPlan& pl, int cta) : items(pl.items), w(cta_work(pl, cta)) {
-    if (w.unit < w.end) next_item = items[w.item];
-  }
+  // (the first record is the CTA's own copy, so that nothing waits for its index)
+  __device__ ItemWalk(const PagesPlan& pl, int cta) : items(pl.items), w(cta_work(pl, cta)), next_item(pl.cta_first[cta]) {}
   __device__ bool next(PageItem* it) {
     if (w.unit >= w.end) return false;
     *it = next_item;
@@ -229,15 +228,16 @@ struct ItemWalk {
 // a call was cut short on, and not on a buffer that holds no plan for these
 // sizes.
 __device__ __forceinline__ bool plan_usable(const PagesView& p, const PagesPlan& pl) {
-  if (pages_raised(p)) {
-    if (threadIdx.x == 0) pl.head->stale = 1;
-    return false;
+  const bool raised = *reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0;
+  const bool other = *reinterpret_cast<volatile const int*>(&pl.head->stale) != 0 || pl.head->key != pl.key;
+  if (!__syncthreads_or(raised || other)) return true;
+  if (threadIdx.x == 0) {
+    if (raised)
+      pl.head->stale = 1;
+    else if (other)
+      raise_error(p.st, ERR_STALE_PLAN, 89);
   }
-  if (__syncthreads_or(*reinterpret_cast<volatile const int*>(&pl.head->stale) != 0 || pl.head->key != pl.key)) {
-    if (threadIdx.x == 0) raise_error(p.st, ERR_STALE_PLAN, 89);
-    return false;
-  }
-  return true;
+  return false;
 }
 __device__ __forceinline__ void raise_on_plan(const PagesView& p, const PagesPlan& pl, uint32_t flag, uint32_t where) {
   pl.head->stale = 1;

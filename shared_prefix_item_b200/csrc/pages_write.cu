@@ -34,6 +34,7 @@ int64_t pages_plan_layout(char* base, int64_t n, int64_t n_rows, int n_kv_heads,
   };
   PagesPlan pl;
   pl.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
+  pl.cta_first = reinterpret_cast<PageItem*>(take((int64_t)sizeof(PageItem) * ctas));
   pl.cta_item = reinterpret_cast<int32_t*>(take(4 * ctas));
   pl.arrived = reinterpret_cast<int32_t*>(take(4 * max_items));
   pl.items = reinterpret_cast<PageItem*>(take((int64_t)sizeof(PageItem) * max_items));
@@ -92,16 +93,24 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   __shared__ int s_scan[32];
   __shared__ uint32_t s_err;
   __shared__ unsigned long long s_tiles;
+  __shared__ int4 s_entry[kPlanThreads];  // {sequence, first row, rows, length} of the first entries
   pdl_launch_dependents();
   if (blockIdx.x > 0) {
+    // (not stopped by a raised status: every row gets a record that is safe to
+    // read, whichever CTA raises what)
     pdl_wait();
-    if (pages_raised(p)) return;
+    int32_t* const s_offset = reinterpret_cast<int32_t*>(s_entry);
+    const bool near = b.n <= (int)(sizeof s_entry / 4);
+    if (near)
+      for (int i = threadIdx.x; i < b.n; i += kPlanThreads) s_offset[i] = b.offset[i];
+    __syncthreads();
+    const int32_t* offset = near ? s_offset : b.offset;
     for (int r = (blockIdx.x - 1) * kPlanThreads + threadIdx.x; r < b.n_rows; r += (gridDim.x - 1) * kPlanThreads) {
       // the last entry that begins at or before r
       int lo = 0, hi = b.n;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (b.offset[mid] <= r)
+        if (offset[mid] <= r)
           lo = mid;
         else
           hi = mid;
@@ -128,6 +137,16 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   if (threadIdx.x == 0) s_err = 0, s_tiles = 0;
   __syncthreads();
   pdl_wait();
+  // entries up to kPlanThreads are read once, here
+  int s0 = 0, o0 = 0, rows0 = 0, len0 = 0;
+  uint32_t err0 = 0;
+  const bool ok0 = threadIdx.x < b.n && entry_of(p, b, threadIdx.x, &s0, &o0, &rows0, &len0, &err0);
+  s_entry[threadIdx.x] = make_int4(s0, o0, rows0, len0);
+  auto entry = [&](int i, int* s, int* o, int* rows, int* len, uint32_t* err) {
+    if (i != threadIdx.x) return entry_of(p, b, i, s, o, rows, len, err);
+    *s = s0, *o = o0, *rows = rows0, *len = len0, *err = err0;
+    return ok0;
+  };
   if (pages_raised(p)) {
     if (threadIdx.x == 0) pl.head->stale = 1;
     return;
@@ -137,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   for (int i = threadIdx.x; i < b.n; i += kPlanThreads) {
     int s, o, rows, len;
     uint32_t err = 0;
-    if (!entry_of(p, b, i, &s, &o, &rows, &len, &err)) continue;
+    if (!entry(i, &s, &o, &rows, &len, &err)) continue;
     unsigned long long u = 0;
     for (int t = 0; t < rows; t += m) u += key_tiles(item_keys(b, rows, len, t, m), keys);
     atomicAdd(&s_tiles, u * p.n_kv_heads);
@@ -152,7 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
     if (i < b.n) {
       int s, o, rows, len;
       uint32_t err = 0;
-      const bool ok = entry_of(p, b, i, &s, &o, &rows, &len, &err);
+      const bool ok = entry(i, &s, &o, &rows, &len, &err);
       if (!ok || (i == 0 && o != 0)) {
         atomicOr(&s_err, ok ? (uint32_t)ERR_BAD_LENGTH : err);
       } else if (!claim(seen, s)) {
@@ -194,7 +213,12 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   for (int i = threadIdx.x >> 5; i < b.n; i += kPlanThreads / 32) {
     int s, o, rows, len;
     uint32_t err;
-    entry_of(p, b, i, &s, &o, &rows, &len, &err);
+    if (i < kPlanThreads) {
+      const int4 e = s_entry[i];
+      s = e.x, o = e.y, rows = e.z, len = e.w;
+    } else {
+      entry_of(p, b, i, &s, &o, &rows, &len, &err);
+    }
     const int2 base = pl.base[i];
     const int tiles = (rows + m - 1) / m;
     int per_head = 0;  // units of one head's items
@@ -233,7 +257,9 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
           for (int c = unit_cta(it.unit0, units, ctas); c < ctas; ++c) {
             const int first = cta_unit(c, units, ctas);
             if (first >= it.unit0 + u) break;
-            if (first >= it.unit0) pl.cta_item[c] = k;
+            if (first < it.unit0) continue;
+            pl.cta_item[c] = k;
+            pl.cta_first[c] = it;
           }
         }
       before += __shfl_sync(0xffffffffu, x, 31);
@@ -471,7 +497,7 @@ extern "C" int duolm_pages_plan(const duolm_pages* pages, const duolm_pages_batc
   const size_t smem = (size_t)((p.n_seqs + 31) / 32) * 4;
   const int grid = 1 + std::min((batch->n_rows + kPlanThreads - 1) / kPlanThreads, sms - 1);
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024 - 512)
+  if (smem > 24 * 1024)  // with 17 KB of its own
     e = cudaFuncSetAttribute(batch_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
   if (e == cudaSuccess)
     e = launch_ex(batch_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(cuda_stream), true,
