@@ -503,7 +503,7 @@ int duolm_pages_plan(const duolm_pages *pages, const duolm_pages_batch *batch, v
 /*
  * duolm_pages_write: a layer's projections into the cache.  Every q and k head
  * is RMS-normalised over head_dim (gains q_gain, k_gain: device float
- * [head_dim], NULL: no norm) and its pairs (i, i + head_dim / 2) are rotated
+ * [head_dim], 16-byte aligned, NULL: no norm) and its pairs (i, i + head_dim / 2) are rotated
  * by rope[position][i] = (cos, sin) (device float [rope_positions][head_dim /
  * 2][2], 16-byte aligned, NULL: no rotation), in fp32, rounded once.  k goes
  * to its token's slot, v there unchanged, q to q_out (which may be q).

@@ -81,6 +81,39 @@ __device__ __forceinline__ int block_scan(int v, int* s, int* total) {
   return before + x - v;
 }
 
+// The same of three values at once (kPlanThreads threads, s[3][32]).
+__device__ __forceinline__ void block_scan3(const int (&v)[3], int (*s)[32], int (&before)[3], int (&total)[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x[3] = {v[0], v[1], v[2]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] = min(x[k] + y, kScanCap);
+    }
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (lane == 31) s[k][warp] = x[k];
+  __syncthreads();
+  if (warp < 3) {
+    int y = s[warp][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y = min(y + z, kScanCap);
+    }
+    s[warp][lane] = y;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    before[k] = (warp ? s[k][warp - 1] : 0) + x[k] - v[k];
+    total[k] = s[k][31];
+  }
+  __syncthreads();
+}
+
 // true for the first call with this id in the block
 __device__ __forceinline__ bool claim(uint32_t* seen, int id) {
   return !(atomicOr(&seen[id >> 5], 1u << (id & 31)) >> (id & 31) & 1u);
@@ -162,7 +195,7 @@ struct PagesPlan {
   int32_t* cta_item;
   int32_t* arrived;   // [max_items] finished parts of a divided item (0 between calls)
   PageItem* items;    // [max_items]
-  int2* base;         // [n + 1] per entry: items and units before it
+  int4* base;         // [n] per entry: items and units before it (of more entries than one CTA holds)
   int2* rows;         // [n_rows] {page * page_tokens + slot, position}; x: kRowNone, kRowOutside
   float* parts;       // [2 ctas][part_words]
   int max_items, ctas;

@@ -2,6 +2,8 @@
 // the projections (QK-norm, rotary positions, K and V into their pages).
 #include "pages.cuh"
 
+#include <type_traits>
+
 namespace duolm {
 
 PagesPath pages_path(int dtype, int64_t max_rows, int group) {
@@ -38,7 +40,7 @@ int64_t pages_plan_layout(char* base, int64_t n, int64_t n_rows, int n_kv_heads,
   pl.cta_item = reinterpret_cast<int32_t*>(take(4 * ctas));
   pl.arrived = reinterpret_cast<int32_t*>(take(4 * max_items));
   pl.items = reinterpret_cast<PageItem*>(take((int64_t)sizeof(PageItem) * max_items));
-  pl.base = reinterpret_cast<int2*>(take(8 * n));
+  pl.base = reinterpret_cast<int4*>(take(16 * n));
   pl.rows = reinterpret_cast<int2*>(take(8 * n_rows));
   pl.parts = reinterpret_cast<float*>(take(2ll * ctas * sh.part_words * 4));
   pl.max_items = (int)max_items;
@@ -85,185 +87,166 @@ __device__ __forceinline__ int item_keys(const BatchView& b, int rows, int len, 
 
 __device__ __forceinline__ int key_tiles(int n_keys, int keys) { return max(1, (n_keys + keys - 1) / keys); }  // one at least: an item that sees no key still writes its rows
 
-// CTA 0: the attention's items and how the CTAs divide their key tiles.  The
-// other CTAs: where each query row's token lies in the cache.
+// The plan: the attention's items, how the CTAs divide their key tiles, and
+// where each query row's token lies in the cache.  Every CTA reads the entries
+// and sums their items and units for itself (up to kPlanThreads entries, from
+// registers and shared memory); then items and rows are a thread's work each,
+// spread over the grid.  With more entries one CTA alone makes the items, from
+// sums in memory.  A chain of dependent loads bounds it: one CTA making the
+// items of 64 entries, a warp to an entry, took 24 us.
 __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, BatchView b, PagesPlan pl, int m,
                                                                   int keys, int grain) {
   extern __shared__ uint32_t seen[];
-  __shared__ int s_scan[32];
+  __shared__ int s_scan[3][32];
   __shared__ uint32_t s_err;
-  __shared__ unsigned long long s_tiles;
-  __shared__ int4 s_entry[kPlanThreads];  // {sequence, first row, rows, length} of the first entries
+  __shared__ int4 s_entry[kPlanThreads];  // {sequence, first row, rows, length}
+  __shared__ int4 s_base[kPlanThreads];   // {items, units of one tile, units of `grain` tiles} of the entries before
   pdl_launch_dependents();
-  if (blockIdx.x > 0) {
-    // (not stopped by a raised status: every row gets a record that is safe to
-    // read, whichever CTA raises what)
-    pdl_wait();
-    int32_t* const s_offset = reinterpret_cast<int32_t*>(s_entry);
-    const bool near = b.n <= (int)(sizeof s_entry / 4);
-    if (near)
-      for (int i = threadIdx.x; i < b.n; i += kPlanThreads) s_offset[i] = b.offset[i];
-    __syncthreads();
-    const int32_t* offset = near ? s_offset : b.offset;
-    for (int r = (blockIdx.x - 1) * kPlanThreads + threadIdx.x; r < b.n_rows; r += (gridDim.x - 1) * kPlanThreads) {
-      // the last entry that begins at or before r
-      int lo = 0, hi = b.n;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (offset[mid] <= r)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      int s, o, rows, len;
-      uint32_t err;
-      int2 at = make_int2(kRowNone, 0);
-      if (entry_of(p, b, lo, &s, &o, &rows, &len, &err) && r >= o && r < o + rows) {
-        const int pos = len - rows + r - o;
-        at.x = kRowOutside;
-        if (pos >= 0) {
-          const int page = p.table[(int64_t)s * p.max_pages + (pos >> p.page_shift)];
-          if ((unsigned)page < (unsigned)p.n_pages)
-            at = make_int2((page << p.page_shift) + (pos & (p.page_tokens - 1)), pos);
-          else
-            raise_error(p.st, ERR_BAD_INDEX, 88);
-        }
-      }
-      pl.rows[r] = at;
-    }
-    return;
-  }
-  for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
-  if (threadIdx.x == 0) s_err = 0, s_tiles = 0;
+  const int tid = threadIdx.x;
+  const bool near = b.n <= kPlanThreads, makes_items = near || blockIdx.x == 0;
+  for (int i = tid; i < (p.n_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
+  if (tid == 0) s_err = 0;
   __syncthreads();
   pdl_wait();
-  // entries up to kPlanThreads are read once, here
-  int s0 = 0, o0 = 0, rows0 = 0, len0 = 0;
-  uint32_t err0 = 0;
-  const bool ok0 = threadIdx.x < b.n && entry_of(p, b, threadIdx.x, &s0, &o0, &rows0, &len0, &err0);
-  s_entry[threadIdx.x] = make_int4(s0, o0, rows0, len0);
-  auto entry = [&](int i, int* s, int* o, int* rows, int* len, uint32_t* err) {
-    if (i != threadIdx.x) return entry_of(p, b, i, s, o, rows, len, err);
-    *s = s0, *o = o0, *rows = rows0, *len = len0, *err = err0;
-    return ok0;
-  };
-  if (pages_raised(p)) {
-    if (threadIdx.x == 0) pl.head->stale = 1;
-    return;
-  }
-  // A batch of few tiles is divided in units of several: a CTA then takes
-  // longer over them, but fewer items are divided and joined.
-  for (int i = threadIdx.x; i < b.n; i += kPlanThreads) {
-    int s, o, rows, len;
-    uint32_t err = 0;
-    if (!entry(i, &s, &o, &rows, &len, &err)) continue;
-    unsigned long long u = 0;
-    for (int t = 0; t < rows; t += m) u += key_tiles(item_keys(b, rows, len, t, m), keys);
-    atomicAdd(&s_tiles, u * p.n_kv_heads);
-  }
-  __syncthreads();
-  if (s_tiles > (unsigned long long)pl.ctas * grain) grain = 1;
-  const int unit_keys = keys * grain;
-  int items = 0, units = 0;
-  for (int i0 = 0; i0 < b.n; i0 += kPlanThreads) {
-    const int i = i0 + threadIdx.x;
-    int n_it = 0, n_un = 0;
+  // Only CTA 0 heeds a raised status, and marks the plan: what the others write
+  // is safe to read whichever CTA raises what.
+  const bool raised = *reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0;
+  int items = 0, units[2] = {0, 0};
+  for (int i0 = 0; makes_items && i0 < b.n; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int v[3] = {0, 0, 0};
     if (i < b.n) {
       int s, o, rows, len;
       uint32_t err = 0;
-      const bool ok = entry(i, &s, &o, &rows, &len, &err);
+      const bool ok = entry_of(p, b, i, &s, &o, &rows, &len, &err);
+      if (near) s_entry[i] = make_int4(s, o, rows, len);
       if (!ok || (i == 0 && o != 0)) {
         atomicOr(&s_err, ok ? (uint32_t)ERR_BAD_LENGTH : err);
       } else if (!claim(seen, s)) {
         atomicOr(&s_err, ERR_BAD_SEQ);
       } else {
         const int tiles = (rows + m - 1) / m;
-        int64_t u = 0;
-        for (int t = 0; t < tiles; ++t) u += key_tiles(item_keys(b, rows, len, t * m, m), unit_keys);
-        n_it = tiles * p.n_kv_heads;
-        n_un = (int)min(u * p.n_kv_heads, (int64_t)kScanCap);
+        int64_t u1 = 0, ug = 0;
+        for (int t = 0; t < tiles; ++t) {
+          const int k = key_tiles(item_keys(b, rows, len, t * m, m), keys);
+          u1 += k;
+          ug += (k + grain - 1) / grain;
+        }
+        v[0] = tiles * p.n_kv_heads;
+        v[1] = (int)min(u1 * p.n_kv_heads, (int64_t)kScanCap);
+        v[2] = (int)min(ug * p.n_kv_heads, (int64_t)kScanCap);
       }
     }
-    int all_it, all_un;
-    const int it = block_scan(n_it, s_scan, &all_it), un = block_scan(n_un, s_scan, &all_un);
-    if (i < b.n) pl.base[i] = make_int2(items + it, units + un);
-    items = min(items + all_it, kScanCap);
-    units = min(units + all_un, kScanCap);
+    int before[3], all[3];
+    block_scan3(v, s_scan, before, all);
+    if (i < b.n) {
+      const int4 x = make_int4(items + before[0], units[0] + before[1], units[1] + before[2], 0);
+      if (near)
+        s_base[i] = x;
+      else
+        pl.base[i] = x;
+    }
+    items = min(items + all[0], kScanCap);
+    units[0] = min(units[0] + all[1], kScanCap);
+    units[1] = min(units[1] + all[2], kScanCap);
   }
   __syncthreads();
-  if (s_err || units >= kScanCap || items > pl.max_items) {
-    if (threadIdx.x == 0) {
-      raise_error(p.st, s_err ? s_err : (uint32_t)ERR_BAD_LENGTH, 86);
-      pl.head->n_items = pl.head->units = pl.head->ctas = 0;
-      pl.head->stale = 1;
+  // A batch of few tiles is divided in units of several: a CTA then takes
+  // longer over them, but fewer items are divided and joined.
+  const bool coarse = units[0] <= pl.ctas * grain;
+  const int total = coarse ? units[1] : units[0], ctas = min(pl.ctas, total);
+  if (!coarse) grain = 1;
+  const bool refused = s_err || units[0] >= kScanCap || items > pl.max_items;
+  if (blockIdx.x == 0 && tid == 0) {
+    PlanHead& h = *pl.head;
+    if (refused) raise_error(p.st, s_err ? s_err : (uint32_t)ERR_BAD_LENGTH, 86);
+    h.n_items = refused ? 0 : items;
+    h.units = refused ? 0 : total;
+    h.ctas = refused ? 0 : ctas;
+    h.grain = grain;
+    h.key = pl.key;
+    h.stale = raised || refused;
+  }
+  if (makes_items && !refused)
+    for (int k = (near ? blockIdx.x : 0) * kPlanThreads + tid; k < items; k += (near ? gridDim.x : 1) * kPlanThreads) {
+      const int4* base = near ? s_base : pl.base;
+      int lo = 0, hi = b.n;  // the last entry that begins at or before item k
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (base[mid].x <= k)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      int s, o, rows, len;
+      uint32_t err;
+      if (near) {
+        const int4 e = s_entry[lo];
+        s = e.x, o = e.y, rows = e.z, len = e.w;
+      } else {
+        entry_of(p, b, lo, &s, &o, &rows, &len, &err);
+      }
+      const int4 here = base[lo];
+      const int first_unit = coarse ? here.z : here.y;
+      const int end_unit = lo + 1 < b.n ? (coarse ? base[lo + 1].z : base[lo + 1].y) : total;
+      const int tiles = (rows + m - 1) / m, h = (k - here.x) / tiles, t = (k - here.x) % tiles;
+      auto units_of = [&](int t2) { return (key_tiles(item_keys(b, rows, len, t2 * m, m), keys) + grain - 1) / grain; };
+      int before = 0;
+      if (b.causal)
+        for (int t2 = 0; t2 < t; ++t2) before += units_of(t2);
+      else
+        before = t * units_of(0);
+      PageItem it;
+      it.seq = s;
+      it.kv_head = h;
+      it.row0 = o + t * m;
+      it.n_rows = min(m, rows - t * m);
+      it.last0 = b.causal ? len - rows + t * m : 0;
+      it.n_keys = item_keys(b, rows, len, t * m, m);
+      it.unit0 = first_unit + h * ((end_unit - first_unit) / p.n_kv_heads) + before;
+      it.n_tiles = key_tiles(it.n_keys, keys);
+      pl.items[k] = it;
+      pl.arrived[k] = 0;
+      // CTAs whose first unit is in this item
+      const int end = it.unit0 + units_of(t);
+      for (int c = unit_cta(it.unit0, total, ctas); c < ctas; ++c) {
+        const int first = cta_unit(c, total, ctas);
+        if (first >= end) break;
+        if (first < it.unit0) continue;
+        pl.cta_item[c] = k;
+        pl.cta_first[c] = it;
+      }
     }
-    return;
-  }
-  const int ctas = min(pl.ctas, units);
-  if (threadIdx.x == 0) {
-    pl.head->n_items = items;
-    pl.head->units = units;
-    pl.head->ctas = ctas;
-    pl.head->stale = 0;
-    pl.head->key = pl.key;
-    pl.head->grain = grain;
-  }
-  for (int i = threadIdx.x; i < items; i += kPlanThreads) pl.arrived[i] = 0;
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < b.n; i += kPlanThreads / 32) {
+  for (int r = blockIdx.x * kPlanThreads + tid; r < b.n_rows; r += gridDim.x * kPlanThreads) {
+    int lo = 0, hi = b.n;  // the last entry that begins at or before r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((near ? s_entry[mid].y : b.offset[mid]) <= r)
+        lo = mid;
+      else
+        hi = mid;
+    }
     int s, o, rows, len;
     uint32_t err;
-    if (i < kPlanThreads) {
-      const int4 e = s_entry[i];
+    if (near) {
+      const int4 e = s_entry[lo];
       s = e.x, o = e.y, rows = e.z, len = e.w;
     } else {
-      entry_of(p, b, i, &s, &o, &rows, &len, &err);
+      entry_of(p, b, lo, &s, &o, &rows, &len, &err);
     }
-    const int2 base = pl.base[i];
-    const int tiles = (rows + m - 1) / m;
-    int per_head = 0;  // units of one head's items
-    for (int t0 = 0; t0 < tiles; t0 += 32) {
-      const int t = t0 + lane;
-      int u = t < tiles ? key_tiles(item_keys(b, rows, len, t * m, m), unit_keys) : 0;
-#pragma unroll
-      for (int o2 = 16; o2 > 0; o2 >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o2);
-      per_head += u;
-    }
-    int before = 0;
-    for (int t0 = 0; t0 < tiles; t0 += 32) {
-      const int t = t0 + lane;
-      const int nk = t < tiles ? item_keys(b, rows, len, t * m, m) : 0;
-      const int u = t < tiles ? key_tiles(nk, unit_keys) : 0;
-      int x = u;
-#pragma unroll
-      for (int o2 = 1; o2 < 32; o2 <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o2);
-        if (lane >= o2) x += y;
+    int2 at = make_int2(kRowNone, 0);
+    if (r >= o && r < o + rows) {
+      const int pos = len - rows + r - o;
+      at.x = kRowOutside;
+      if (pos >= 0) {
+        const int page = p.table[(int64_t)s * p.max_pages + (pos >> p.page_shift)];
+        if ((unsigned)page < (unsigned)p.n_pages)
+          at = make_int2((page << p.page_shift) + (pos & (p.page_tokens - 1)), pos);
+        else
+          raise_error(p.st, ERR_BAD_INDEX, 88);
       }
-      if (t < tiles)
-        for (int h = 0; h < p.n_kv_heads; ++h) {
-          PageItem it;
-          it.seq = s;
-          it.kv_head = h;
-          it.row0 = o + t * m;
-          it.n_rows = min(m, rows - t * m);
-          it.last0 = b.causal ? len - rows + t * m : 0;
-          it.n_keys = nk;
-          it.unit0 = base.y + h * per_head + before + x - u;
-          it.n_tiles = key_tiles(nk, keys);
-          const int k = base.x + h * tiles + t;
-          pl.items[k] = it;
-          // CTAs whose first unit is in this item
-          for (int c = unit_cta(it.unit0, units, ctas); c < ctas; ++c) {
-            const int first = cta_unit(c, units, ctas);
-            if (first >= it.unit0 + u) break;
-            if (first < it.unit0) continue;
-            pl.cta_item[c] = k;
-            pl.cta_first[c] = it;
-          }
-        }
-      before += __shfl_sync(0xffffffffu, x, 31);
     }
+    pl.rows[r] = at;
   }
 }
 
@@ -287,27 +270,32 @@ struct WriteArgs {
   float eps;
 };
 
+// two elements of a 16-byte word as fp32, and back (one rounding)
 template <typename T>
-__device__ __forceinline__ float elem_f32(T x);
-template <>
-__device__ __forceinline__ float elem_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float elem_f32<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float elem_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float2 pair_f32(const uint4& w, int j) {
+  const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
+  if constexpr (sizeof(T) == 4)
+    return make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+  else if constexpr (std::is_same_v<T, __half>)
+    return __half22float2(*reinterpret_cast<const __half2*>(x + j));
+  else
+    return make_float2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u));
+}
 template <typename T>
-__device__ __forceinline__ T f32_elem(float x);
-template <>
-__device__ __forceinline__ float f32_elem<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half f32_elem<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 f32_elem<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+__device__ __forceinline__ void f32_pair(uint4& w, int j, float2 v) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+  if constexpr (sizeof(T) == 4) {
+    x[2 * j] = __float_as_uint(v.x);
+    x[2 * j + 1] = __float_as_uint(v.y);
+  } else {
+    x[j] = std::is_same_v<T, __half> ? pack_half2(v.x, v.y) : pack_bf162(v.x, v.y);
+  }
+}
 
 template <typename T, int SEG, int U>
 __global__ void __launch_bounds__(256) pages_write_kernel(PagesView p, PagesPlan pl, WriteArgs a) {
-  constexpr int E = 16 / sizeof(T);   // elements of a 16-byte word
-  constexpr int HPW = 32 / SEG;       // heads a warp holds at a time
+  constexpr int E = 16 / sizeof(T), J = E / 2;  // elements, and pairs of them, of a 16-byte word
+  constexpr int HPW = 32 / SEG;                 // heads a warp holds at a time
   pdl_launch_dependents();
   pdl_wait();
   if (!plan_usable(p, pl)) return;
@@ -321,12 +309,7 @@ __global__ void __launch_bounds__(256) pages_write_kernel(PagesView p, PagesPlan
   for (int64_t w = warp; w < (int64_t)a.n_rows * groups; w += warps) {
     const int row = (int)(w / groups), h0 = (int)(w % groups) * (U * HPW);
     const int2 at = pl.rows[row];
-    if (at.x == kRowNone) continue;
-    if (at.x < 0 || (a.rope && at.y >= a.rope_positions)) {
-      raise_error(p.st, ERR_BAD_LENGTH, 87);
-      continue;
-    }
-    uint4 lo[U], hi[U];
+    uint4 lo[U], hi[U];  // (on their way while the row's record is)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * HPW + seg;
@@ -341,15 +324,19 @@ __global__ void __launch_bounds__(256) pages_write_kernel(PagesView p, PagesPlan
       lo[u] = __ldcs(reinterpret_cast<const uint4*>(src) + sl);
       hi[u] = __ldcs(reinterpret_cast<const uint4*>(src + half * sizeof(T)) + sl);
     }
-    float c[E], s[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) c[e] = 1.f, s[e] = 0.f;
+    if (at.x == kRowNone) continue;
+    if (at.x < 0 || (a.rope && at.y >= a.rope_positions)) {
+      raise_error(p.st, ERR_BAD_LENGTH, 87);
+      continue;
+    }
+    float2 c[J], s[J];
     if (a.rope && in) {
       const float4* r = reinterpret_cast<const float4*>(a.rope + (int64_t)at.y * half + sl * E);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const float4 x = r[e];
-        c[2 * e] = x.x, s[2 * e] = x.y, c[2 * e + 1] = x.z, s[2 * e + 1] = x.w;
+      for (int j = 0; j < J; ++j) {
+        const float4 x = r[j];
+        c[j] = make_float2(x.x, x.z);
+        s[j] = make_float2(x.y, x.w);
       }
     }
 #pragma unroll
@@ -357,39 +344,51 @@ __global__ void __launch_bounds__(256) pages_write_kernel(PagesView p, PagesPlan
       const int h = h0 + u * HPW + seg;
       const bool mine = h < n_heads && in;
       const bool is_q = h < q_heads, is_v = h >= q_heads + p.n_kv_heads;
-      float x[2 * E];
-      float ss = 0.f;
-      if (mine) {
-        const T* l = reinterpret_cast<const T*>(&lo[u]);
-        const T* g = reinterpret_cast<const T*>(&hi[u]);
+      const float* gain = is_q ? a.q_gain : a.k_gain;
+      if (__any_sync(0xffffffffu, mine && !is_v && (gain || a.rope))) {
+        float2 x[J], y[J];
+        float2 ss = make_float2(0.f, 0.f);
+        if (mine) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = elem_f32<T>(l[e]), x[E + e] = elem_f32<T>(g[e]);
+          for (int j = 0; j < J; ++j) {
+            x[j] = pair_f32<T>(lo[u], j);
+            y[j] = pair_f32<T>(hi[u], j);
+            ss = ffma2(x[j], x[j], ss);
+            ss = ffma2(y[j], y[j], ss);
+          }
+        }
+        float sum = ss.x + ss.y;
 #pragma unroll
-        for (int e = 0; e < 2 * E; ++e) ss += x[e] * x[e];
+        for (int o = SEG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (mine && !is_v && (gain || a.rope)) {
+          float2 r2 = make_float2(1.f, 1.f);
+          if (gain) {
+            r2.x = r2.y = rsqrtf(sum * inv_hd + a.eps);
+            const float4* gl = reinterpret_cast<const float4*>(gain + sl * E);
+            const float4* gh = reinterpret_cast<const float4*>(gain + half + sl * E);
+#pragma unroll
+            for (int j = 0; j < J; j += 2) {
+              const float4 l4 = __ldg(gl + j / 2), h4 = __ldg(gh + j / 2);
+              x[j] = fmul2(x[j], make_float2(l4.x, l4.y));
+              x[j + 1] = fmul2(x[j + 1], make_float2(l4.z, l4.w));
+              y[j] = fmul2(y[j], make_float2(h4.x, h4.y));
+              y[j + 1] = fmul2(y[j + 1], make_float2(h4.z, h4.w));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            if (a.rope) {
+              const float2 cr = fmul2(c[j], r2), sr = fmul2(s[j], r2);
+              f32_pair<T>(lo[u], j, ffma2(y[j], make_float2(-sr.x, -sr.y), fmul2(x[j], cr)));
+              f32_pair<T>(hi[u], j, ffma2(x[j], sr, fmul2(y[j], cr)));
+            } else {
+              f32_pair<T>(lo[u], j, fmul2(x[j], r2));
+              f32_pair<T>(hi[u], j, fmul2(y[j], r2));
+            }
+          }
+        }
       }
-#pragma unroll
-      for (int o = SEG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (!mine) continue;
-      if (!is_v) {
-        const float* gain = is_q ? a.q_gain : a.k_gain;
-        if (gain) {
-          const float r = rsqrtf(ss * inv_hd + a.eps);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            x[e] *= r * gain[sl * E + e];
-            x[E + e] *= r * gain[half + sl * E + e];
-          }
-        }
-        T* l = reinterpret_cast<T*>(&lo[u]);
-        T* g = reinterpret_cast<T*>(&hi[u]);
-        if (a.rope || gain) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            l[e] = f32_elem<T>(x[e] * c[e] - x[E + e] * s[e]);
-            g[e] = f32_elem<T>(x[E + e] * c[e] + x[e] * s[e]);
-          }
-        }
-      }
       char* dst;
       if (is_q) {
         dst = a.q_out + ((int64_t)row * a.q_out_stride + (int64_t)h * p.head_dim) * sizeof(T);
@@ -413,7 +412,7 @@ cudaError_t write_seg(const PagesView& p, const PagesPlan& pl, const WriteArgs& 
   // below, one, so that few rows spread over more warps
   const int64_t wide = (int64_t)a.n_rows * ((n_heads + U * HPW - 1) / (U * HPW));
   if (wide >= 16ll * sms) {
-    const int grid = (int)std::min<int64_t>((wide + 7) / 8, 8ll * sms);
+    const int grid = (int)std::min<int64_t>((wide + 7) / 8, 2ll * sms);  // what is resident
     return launch_ex(pages_write_kernel<T, SEG, U>, dim3(grid), dim3(256), 0, s, true, p, pl, a);
   }
   const int64_t narrow = (int64_t)a.n_rows * ((n_heads + HPW - 1) / HPW);
@@ -495,9 +494,10 @@ extern "C" int duolm_pages_plan(const duolm_pages* pages, const duolm_pages_batc
   const PathShape sh = pages_path_shape(path, p.head_dim);
   const BatchView b{batch->seq, batch->offset, batch->n, batch->n_rows, group, batch->causal != 0};
   const size_t smem = (size_t)((p.n_seqs + 31) / 32) * 4;
-  const int grid = 1 + std::min((batch->n_rows + kPlanThreads - 1) / kPlanThreads, sms - 1);
+  // a CTA per kPlanThreads rows, and per half as many items, which take longer
+  const int grid = std::min(std::max((batch->n_rows + kPlanThreads - 1) / kPlanThreads, (2 * pl.max_items + kPlanThreads - 1) / kPlanThreads), sms);
   cudaError_t e = cudaSuccess;
-  if (smem > 24 * 1024)  // with 17 KB of its own
+  if (smem > 14 * 1024)  // with 33 KB of its own
     e = cudaFuncSetAttribute(batch_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
   if (e == cudaSuccess)
     e = launch_ex(batch_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(cuda_stream), true,
@@ -522,8 +522,8 @@ extern "C" int duolm_pages_write(const duolm_pages* pages, const duolm_pages_bat
     return pages_fail(DUOLM_E_ARG, "pages_write: a row stride below the row's elements");
   if (misaligned(k, k_stride, p.elem) || misaligned(v, v_stride, p.elem) ||
       (q && (misaligned(q, q_stride, p.elem) || misaligned(q_out, q_out_stride, p.elem))) ||
-      (reinterpret_cast<uintptr_t>(rope) & 15))
-    return pages_fail(DUOLM_E_ARG, "pages_write: rows and the rotation table must be 16-byte aligned");
+      ((reinterpret_cast<uintptr_t>(rope) | reinterpret_cast<uintptr_t>(q_gain) | reinterpret_cast<uintptr_t>(k_gain)) & 15))
+    return pages_fail(DUOLM_E_ARG, "pages_write: rows, gains and the rotation table must be 16-byte aligned");
   if (rope && rope_positions < 1) return pages_fail(DUOLM_E_ARG, "pages_write: empty rotation table");
   if (!(eps >= 0.f)) return pages_fail(DUOLM_E_ARG, "pages_write: eps %g", eps);
   if ((rc = batch_layout(pages, p, batch, &pl, &path, &sms))) return rc;
