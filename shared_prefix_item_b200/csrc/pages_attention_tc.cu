@@ -18,14 +18,23 @@
 // One CTA per SM, 384 threads:
 //   warps 0-3 softmax of A, 4-7 of B: a thread holds a row (its TMEM lane) and
 //             128 keys;
-//   warp 8    TMA: Q (one box of the entry's rows x the heads of the group),
-//             then K and V page by page, a lane to each box; 128-byte swizzle;
+//   warp 8    TMA of K page by page, a lane to each box; 128-byte swizzle;
+//   warp 11   TMA of Q (one box of the entry's rows x the heads of the group; an
+//             item of one sub-tile leaves the other buffer for the next item's)
+//             and of V;
 //   warp 9    one lane issues tcgen05.mma, per tile first O_X += P_X V of the
 //             chain's previous tile (P read from tensor memory), then S_X;
-//   warp 10   V rows behind the last visible key are zeroed in shared memory
-//             before the tensor core reads them: P is 0 there, but the slots may
-//             hold anything, and 0 x NaN is NaN;
-//   warp 11   idle.
+//   warp 10   relays arrivals: P_X counts as full when the softmax has stored it
+//             and this warp has seen V of its tile, so that the issuing thread
+//             has one wait where it had two.  That thread bounds the kernel: a
+//             wait or commit costs it 100 to 200 cycles in which no product
+//             runs, eight products cost 512.  The warp also zeroes V rows behind
+//             the last visible key: P is 0 there, but the slots may hold
+//             anything, and 0 x NaN is NaN.
+// A step is what the issuer does for one K/V tile; one commit at its end frees
+// K of this step's tile and V of the tiles whose P V it ran.  A barrier's phase
+// can be waited for only while it is the current or the last one, so one warp
+// (8) sees every step in turn and tells warp 11 which V slots are free.
 // Tensor memory: S/P of A in columns [0, 128), of B in [128, 256), O of A from
 // 256, of B from 384.  tcgen05.mma of one thread run in issue order, so S_X may
 // be issued right behind the P V that reads the same columns, and its commit
@@ -40,7 +49,7 @@ namespace {
 
 constexpr int kSub = 128, kKeys = 128;
 constexpr int kWG = 128, kThreads = 3 * kWG;
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpTail = 10;
+constexpr int kWarpK = 8, kWarpMma = 9, kWarpRelay = 10, kWarpQV = 11;
 // registers move from the third warpgroup to the softmax (sum: the launch's 384 x 168)
 constexpr int kRegLaunch = 168, kRegSoftmax = 200, kRegOther = 104;
 static_assert(2 * kWG * kRegSoftmax + kWG * kRegOther <= kThreads * kRegLaunch, "register split above the launch's registers");
@@ -58,11 +67,11 @@ struct Lay {
   static constexpr int SMEM = STAT + 1024 + 1024;
 };
 
-enum { B_QFULL, B_QEMPTY, B_SFULL0, B_SFULL1, B_PFULL0, B_PFULL1, B_OFULL0, B_OFULL1, B_DRAIN, B_KV };
-// then per slot: K full, K empty, V full, V empty, V raw (a tile whose rows are still to be zeroed)
+enum { B_QFULL0, B_QFULL1, B_QEMPTY0, B_QEMPTY1, B_SFULL0, B_SFULL1, B_PFULL0, B_PFULL1, B_OFULL0, B_OFULL1, B_DRAIN, B_KV };
+// then per slot: K full, V full, step done, V free
+enum { KFULL, VFULL, STEP, VFREE };
 template <int HD>
 __device__ __forceinline__ int kv_bar(int kind, uint32_t slot) { return B_KV + kind * Lay<HD>::SLOTS + slot; }
-enum { KFULL, KEMPTY, VFULL, VEMPTY, VRAW };
 
 __device__ __forceinline__ void named_sync(int id) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(2 * kWG) : "memory");
@@ -89,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   auto kvbar = [&](int kind, uint32_t slot) { return smem_u32(bars + kv_bar<HD>(kind, slot)); };
-  constexpr int kBars = B_KV + 5 * SLOTS;
+  constexpr int kBars = B_KV + 4 * SLOTS;
   static_assert(kBars * 8 + 8 <= 256, "barriers");
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kBars);
   int* s_last = reinterpret_cast<int*>(tmem_holder + 1);
@@ -98,11 +107,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.group, sub_tokens = kSub / G;
-  if (warp == kWarpTma && lane == 0) {
+  if (warp == kWarpK && lane == 0) {
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
-    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), (i == B_PFULL0 || i == B_PFULL1) ? (uint32_t)kWG : 1u);
+    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), (i == B_PFULL0 || i == B_PFULL1) ? 4u + 1u : 1u);
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -142,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int lt = first; lt < nt; lt += step, ++n_xt) {
         ok = ok && mbar_wait_warp(bar(B_SFULL0 + X), n_xt & 1u, p.st, 100);
         if (!ok || !live) {
-          mbar_arrive(bar(B_PFULL0 + X));
+          if (lane == 0) mbar_arrive(bar(B_PFULL0 + X));
           continue;
         }
         tc_fence_after();
@@ -204,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(B_PFULL0 + X));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL0 + X));
       }
       // ---- the item's end.  O_X is overwritten only by the P V of the next
       // item's first P, which this warpgroup releases after reading it.
@@ -332,164 +342,186 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) pl.head->stale = 1;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == kWarpTma) {
-      // ---- TMA: a lane to each 64-element box of a page
-      const int box = min(p.page_tokens, kKeys), boxes = kKeys / box * NH;
-      const int bj = lane / NH, bh = lane % NH;
-      uint32_t n_kv = 0, n_it = 0, raw_par = 0, raw_last = 0;
+    // a K or V tile: a lane to each 64-element box of a page
+    const int box = min(p.page_tokens, kKeys), boxes = kKeys / box * NH;
+    const int bj = lane / NH, bh = lane % NH;
+    auto fetch = [&](int t) {  // page of the lane's box of tile t
+      const int key = t * kKeys + bj * box;
+      return lane < boxes && key < it.n_keys ? p.table[(int64_t)it.seq * p.max_pages + (key >> p.page_shift)] : -1;
+    };
+    auto load_tile = [&](const CUtensorMap* map, int t, int id, uint32_t dst, uint32_t b) {
+      const int left = it.n_keys - t * kKeys;  // keys of this tile
+      const int n_boxes = left <= 0 ? 0 : min(kKeys / box, (left + box - 1) / box) * NH;
+      const bool have = lane < n_boxes;
+      if (have && (unsigned)id >= (unsigned)p.n_pages) {
+        raise_on_plan(p, pl, ERR_BAD_INDEX, 103);
+        id = 0;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(b, n_boxes * box * 128);
+      __syncwarp();
+      if (have)
+        tma_load_2d(map, dst + bh * kHalf + bj * box * 128, b, bh * 64,
+                    ((id * p.n_kv_heads + it.kv_head) << p.page_shift) + ((t * kKeys + bj * box) & (p.page_tokens - 1)));
+    };
+    if (warp == kWarpK) {
+      // n: K tiles loaded; seen: steps seen; nv: V slots handed on; lane i has
+      // the step that frees V of the last tile k with k % 32 == i
+      uint32_t n = 0, seen = 0, nv = 0, frees = 0;
       bool ok = true;
-      for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
-        const int32_t* table = p.table + (int64_t)it.seq * p.max_pages;
-        auto fetch = [&](int t) {
-          const int key = t * kKeys + bj * box;
-          return lane < boxes && key < it.n_keys ? table[key >> p.page_shift] : -1;
-        };
-        const bool two = it.n_rows > sub_tokens;
-        int id = fetch(walk.t0);
-        ok = mbar_wait_warp(bar(B_QEMPTY), (n_it & 1u) ^ 1u, p.st, 102);
-        if (!ok) break;
-        if (lane == 0) {
-          const int subs = two ? 2 : 1;
-          mbar_arrive_expect_tx(bar(B_QFULL), subs * NH * sub_tokens * G * 128);
-          for (int s = 0; s < subs; ++s)
-            for (int h = 0; h < NH; ++h)
-              tma_load_3d(&tmQ, sbase + L::Q + (s * NH + h) * kHalf, bar(B_QFULL), h * 64, it.kv_head * G,
-                          it.row0 + s * sub_tokens);
+      auto free_v = [&]() {
+        while (nv < n && (nv < SLOTS || __shfl_sync(0xffffffffu, frees, (nv - SLOTS) & 31) < seen)) {
+          if (lane == 0) mbar_arrive(kvbar(VFREE, nv % SLOTS));
+          ++nv;
         }
-        ++n_it;
-        for (int t = walk.t0; t < walk.t1; ++t, ++n_kv) {
-          const uint32_t slot = n_kv % SLOTS, par = (n_kv / SLOTS & 1u) ^ 1u;
+      };
+      for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
+        const bool two = it.n_rows > sub_tokens;
+        const uint32_t end = n + (walk.t1 - walk.t0);  // the next item's first step
+        int id = fetch(walk.t0);
+        for (int t = walk.t0; t < walk.t1; ++t) {
+          const uint32_t slot = n % SLOTS;
           const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
-          const int left = it.n_keys - t * kKeys;  // keys of this tile
-          const int n_boxes = left <= 0 ? 0 : min(kKeys / box, (left + box - 1) / box) * NH;
-          const bool have = lane < n_boxes;
-          if (have && (unsigned)id >= (unsigned)p.n_pages) {
-            raise_on_plan(p, pl, ERR_BAD_INDEX, 103);
-            id = 0;
+          if (n >= SLOTS) {
+            if (!(ok = mbar_wait_warp(kvbar(STEP, slot), (n / SLOTS - 1) & 1u, p.st, 104))) break;
+            ++seen;
           }
-          const int y = have ? ((id * p.n_kv_heads + it.kv_head) << p.page_shift) +
-                                   ((t * kKeys + bj * box) & (p.page_tokens - 1))
-                             : 0;
-          const uint32_t off = bh * kHalf + bj * box * 128;
-          if (!(ok = mbar_wait_warp(kvbar(KEMPTY, slot), par, p.st, 104))) break;
-          if (lane == 0) mbar_arrive_expect_tx(kvbar(KFULL, slot), n_boxes * box * 128);
-          __syncwarp();
-          if (have) tma_load_2d(&tmK, sbase + L::K + slot * NH * kHalf + off, kvbar(KFULL, slot), bh * 64, y);
-          raw_last &= ~(1u << slot);
-          if (!(ok = mbar_wait_warp(kvbar(VEMPTY, slot), par, p.st, 105))) {
-            ++n_kv;
-            raw_last |= 1u << (slot + 8);  // K armed, V not
-            break;
-          }
-          const bool tail = left < kKeys;
-          const uint32_t vb = kvbar(tail ? VRAW : VFULL, slot);
-          if (lane == 0) mbar_arrive_expect_tx(vb, n_boxes * box * 128);
-          __syncwarp();
-          if (have) tma_load_2d(&tmV, sbase + L::V + slot * NH * kHalf + off, vb, bh * 64, y);
-          if (tail) {
-            raw_last |= 1u << slot;
-            raw_par ^= 1u << slot;
-          }
+          load_tile(&tmK, t, id, sbase + L::K + slot * NH * kHalf, kvbar(KFULL, slot));
+          if (lane == (int)(n & 31)) frees = two ? n + 1 : min(n + 2, end);
+          ++n;
+          free_v();
           id = next_id;
         }
       }
-      if (!ok && lane == 0) {
-        // leave no copy in flight into shared memory that this CTA gives up
-        if (n_it > 0) mbar_wait(bar(B_QFULL), (n_it - 1) & 1u, p.st, 106);
-        for (uint32_t k = n_kv > SLOTS ? n_kv - SLOTS : 0; k < n_kv; ++k) {
-          const uint32_t slot = k % SLOTS, par = k / SLOTS & 1u;
-          mbar_wait(kvbar(KFULL, slot), par, p.st, 106);
-          if (raw_last >> slot & 1u)
-            mbar_wait(kvbar(VRAW, slot), (raw_par >> slot & 1u) ^ 1u, p.st, 106);
-          else if (!(raw_last >> (slot + 8) & 1u))
-            mbar_wait(kvbar(VFULL, slot), par, p.st, 106);
+      for (; ok && nv < n; free_v()) {
+        if (!(ok = mbar_wait_warp(kvbar(STEP, seen % SLOTS), seen / SLOTS & 1u, p.st, 104))) break;
+        ++seen;
+      }
+      if (!ok)  // leave no copy in flight into shared memory that this CTA gives up
+        for (uint32_t k = n > SLOTS ? n - SLOTS : 0; k < n; ++k)
+          mbar_wait_warp(kvbar(KFULL, k % SLOTS), k / SLOTS & 1u, p.st, 106);
+    } else if (warp == kWarpQV) {
+      uint32_t n = 0, nq = 0;
+      bool ok = true;
+      for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
+        const bool two = it.n_rows > sub_tokens;
+        int id = fetch(walk.t0);
+        for (int s = 0; s < (two ? 2 : 1); ++s, ++nq) {
+          const uint32_t b = nq & 1u;
+          if (!(ok = mbar_wait_warp(bar(B_QEMPTY0 + b), (nq >> 1 & 1u) ^ 1u, p.st, 102))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(B_QFULL0 + b), NH * sub_tokens * G * 128);
+            for (int h = 0; h < NH; ++h)
+              tma_load_3d(&tmQ, sbase + L::Q + (b * NH + h) * kHalf, bar(B_QFULL0 + b), h * 64, it.kv_head * G,
+                          it.row0 + s * sub_tokens);
+          }
+        }
+        for (int t = walk.t0; ok && t < walk.t1; ++t, ++n) {
+          const uint32_t slot = n % SLOTS;
+          const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
+          if (!(ok = mbar_wait_warp(kvbar(VFREE, slot), n / SLOTS & 1u, p.st, 105))) break;
+          load_tile(&tmV, t, id, sbase + L::V + slot * NH * kHalf, kvbar(VFULL, slot));
+          id = next_id;
         }
       }
-    } else if (warp == kWarpTail) {
-      uint32_t n_kv = 0, raw_par = 0;
+      if (!ok) {
+        for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k) mbar_wait_warp(bar(B_QFULL0 + (k & 1)), k >> 1 & 1u, p.st, 106);
+        for (uint32_t k = n > SLOTS ? n - SLOTS : 0; k < n; ++k)
+          mbar_wait_warp(kvbar(VFULL, k % SLOTS), k / SLOTS & 1u, p.st, 106);
+      }
+    } else if (warp == kWarpRelay) {
+      uint32_t n = 0, xt[2] = {0, 0};
       bool ok = true;
-      for (ItemWalk walk(pl, cta); ok && walk.next(&it);)
-        for (int t = walk.t0; t < walk.t1 && ok; ++t, ++n_kv) {
+      for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
+        const bool two = it.n_rows > sub_tokens;
+        for (int t = walk.t0; t < walk.t1 && ok; ++t, ++n) {
+          const uint32_t slot = n % SLOTS;
+          if (!(ok = mbar_wait_warp(kvbar(VFULL, slot), n / SLOTS & 1u, p.st, 107))) break;
           const int left = max(0, it.n_keys - t * kKeys);
-          if (left >= kKeys) continue;
-          const uint32_t slot = n_kv % SLOTS;
-          if (!(ok = mbar_wait_warp(kvbar(VRAW, slot), raw_par >> slot & 1u, p.st, 107))) break;
-          raw_par ^= 1u << slot;
-          uint8_t* v = smem + L::V + slot * NH * kHalf;
-          for (int h = 0; h < NH; ++h)
-            for (int i = left * 8 + lane; i < kKeys * 8; i += 32)
-              *reinterpret_cast<uint4*>(v + h * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+          if (left < kKeys) {
+            uint8_t* v = smem + L::V + slot * NH * kHalf;
+            for (int h = 0; h < NH; ++h)
+              for (int i = left * 8 + lane; i < kKeys * 8; i += 32)
+                *reinterpret_cast<uint4*>(v + h * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+          }
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(kvbar(VFULL, slot));
+#pragma unroll
+          for (int X = 0; X < 2; ++X) {
+            if (!two && X != ((t - walk.t0) & 1)) continue;
+            // the phase before has to be over: this arrival belongs to the next
+            if (xt[X] > 0 && !(ok = mbar_wait_warp(bar(B_PFULL0 + X), (xt[X] - 1) & 1u, p.st, 114))) break;
+            if (lane == 0) mbar_arrive(bar(B_PFULL0 + X));
+            ++xt[X];
+          }
         }
+      }
     } else if (warp == kWarpMma && lane == 0) {
-      // ---- MMA issuer (state in named registers)
-      struct Pending {  // P V of a chain's tile, issued before its next S
-        int valid, first, last, release_v;
-        uint32_t slot, par, xt;
-      };
-      Pending pa{}, pb{};
-      uint32_t n_kv = 0, xt_a = 0, xt_b = 0, n_it = 0;
+      // ---- MMA issuer: one copy of each product's code, the chain a variable
+      constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // 8-row groups, version, 128-byte swizzle
+      auto desc = [](uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; };
+      const uint32_t q_lo = ((sbase + L::Q) >> 4) | 1u << 16, k_lo = ((sbase + L::K) >> 4) | 1u << 16,
+                     v_lo = ((sbase + L::V) >> 4) | (uint32_t)(kHalf >> 4) << 16;
+      // P V of a chain's last tile, issued before its next S: bit 0 there is
+      // one, 1 the item's first tile of the chain, 2 its last, 8.. the slot
+      uint32_t pend_a = 0, pend_b = 0, xt_a = 0, xt_b = 0;  // xt: P V issued
+      uint32_t n = 0, nq = 0;
       bool ok = true;
-      auto issue_pv = [&](int X, Pending& q) -> bool {
-        if (!mbar_wait(bar(B_PFULL0 + X), q.xt & 1u, p.st, 108)) return false;
-        if (!mbar_wait(kvbar(VFULL, q.slot), q.par, p.st, 109)) return false;
+      auto issue_pv = [&](int X, uint32_t pend) -> bool {
+        if (!mbar_wait(bar(B_PFULL0 + X), (X ? xt_b : xt_a) & 1u, p.st, 108)) return false;
         tc_fence_after();
         const uint32_t tS = tmem + 128 * X, tO = tmem + 256 + 128 * X;
-        const uint32_t vbase = sbase + L::V + q.slot * NH * kHalf;
+        const uint32_t v = v_lo + (pend >> 8) * (NH * kHalf >> 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          tc_mma_f16_ts(tO, tS + 8 * k, smem_desc_sw128_mn(vbase + k * 2048, kHalf), kIdescPV, (q.first && k == 0) ? 0u : 1u);
-        if (q.last) tc_commit(bar(B_OFULL0 + X));
-        if (q.release_v) tc_commit(kvbar(VEMPTY, q.slot));
-        q.valid = 0;
+          tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? ~pend & 2u : 1u);
+        if (pend & 4u) tc_commit(bar(B_OFULL0 + X));
+        if (X) ++xt_b; else ++xt_a;
         return true;
-      };
-      auto issue_s = [&](int X, int q_sub, uint32_t slot) {
-        const uint32_t qbase = sbase + L::Q + q_sub * NH * kHalf, kbase = sbase + L::K + slot * NH * kHalf;
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          tc_mma_f16(tmem + 128 * X, smem_desc_sw128(qbase + (k >> 2) * kHalf + (k & 3) * 32),
-                     smem_desc_sw128(kbase + (k >> 2) * kHalf + (k & 3) * 32), kIdescS, k > 0 ? 1u : 0u);
-        tc_commit(bar(B_SFULL0 + X));
       };
       for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
         const bool two = it.n_rows > sub_tokens;
         const int nt = walk.t1 - walk.t0;
-        if (!(ok = mbar_wait(bar(B_QFULL), n_it & 1u, p.st, 110))) break;
-        ++n_it;
-        for (int lt = 0; lt < nt; ++lt, ++n_kv) {
-          const uint32_t slot = n_kv % SLOTS, par = n_kv / SLOTS & 1u;
-          if (!(ok = mbar_wait(kvbar(KFULL, slot), par, p.st, 111))) break;
-          if (two) {
-            if (pa.valid && !(ok = issue_pv(0, pa))) break;
-            tc_fence_after();
-            issue_s(0, 0, slot);
-            pa = Pending{1, lt == 0, lt == nt - 1, 0, slot, par, xt_a++};
-            if (pb.valid && !(ok = issue_pv(1, pb))) break;
-            tc_fence_after();
-            issue_s(1, 1, slot);
-            pb = Pending{1, lt == 0, lt == nt - 1, 1, slot, par, xt_b++};
-          } else if (lt & 1) {
-            if (pb.valid && !(ok = issue_pv(1, pb))) break;
-            tc_fence_after();
-            issue_s(1, 0, slot);
-            pb = Pending{1, lt == 1, lt >= nt - 2, 1, slot, par, xt_b++};
-          } else {
-            if (pa.valid && !(ok = issue_pv(0, pa))) break;
-            tc_fence_after();
-            issue_s(0, 0, slot);
-            pa = Pending{1, lt == 0, lt >= nt - 2, 1, slot, par, xt_a++};
-            // what the last item left of the other chain
-            if (lt == 0 && pb.valid && !(ok = issue_pv(1, pb))) break;
+        for (int lt = 0; lt < nt && ok; ++lt, ++n) {
+          const uint32_t slot = n % SLOTS;
+          ok = mbar_wait(kvbar(KFULL, slot), n / SLOTS & 1u, p.st, 111);
+          if (lt == 0)
+            for (uint32_t b = nq; b < nq + (two ? 2 : 1) && ok; ++b)
+              ok = mbar_wait(bar(B_QFULL0 + (b & 1u)), b >> 1 & 1u, p.st, 110);
+          if (!ok) break;
+          const int subs = two || lt == 0 ? 2 : 1;
+#pragma unroll 1
+          for (int i = 0; i < subs; ++i) {
+            const int X = subs == 2 ? i : lt & 1;
+            uint32_t pend = X ? pend_b : pend_a;
+            if (pend) {
+              if (!(ok = issue_pv(X, pend))) break;
+              pend = 0;
+            }
+            if (two || i == 0) {  // (else: what the last item left of the other chain)
+              tc_fence_after();
+              const uint32_t qb = (nq + (two ? X : 0)) & 1u;
+              const uint32_t q = q_lo + qb * (NH * kHalf >> 4), k0 = k_lo + slot * (NH * kHalf >> 4);
+#pragma unroll
+              for (int k = 0; k < HD / 16; ++k) {
+                const uint32_t o = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+                tc_mma_f16(tmem + 128 * X, desc(q + o), desc(k0 + o), kIdescS, k > 0 ? 1u : 0u);
+              }
+              tc_commit(bar(B_SFULL0 + X));
+              if (lt == nt - 1) tc_commit(bar(B_QEMPTY0 + qb));
+              const int step = two ? 1 : 2;
+              pend = 1u | (lt < step ? 2u : 0u) | (lt + step >= nt ? 4u : 0u) | slot << 8;
+            }
+            if (X)
+              pend_b = pend;
+            else
+              pend_a = pend;
           }
-          tc_commit(kvbar(KEMPTY, slot));
-          if (lt == nt - 1) tc_commit(bar(B_QEMPTY));
+          if (ok) tc_commit(kvbar(STEP, slot));
         }
+        nq += two ? 2 : 1;
       }
-      if (ok && pa.valid) ok = issue_pv(0, pa);
-      if (ok && pb.valid) ok = issue_pv(1, pb);
+      if (ok && pend_a) ok = issue_pv(0, pend_a);
+      if (ok && pend_b) ok = issue_pv(1, pend_b);
       // no tensor-core operation of this CTA may outlive its TMEM
       tc_commit(bar(B_DRAIN));
       mbar_wait(bar(B_DRAIN), 0, p.st, 112);
