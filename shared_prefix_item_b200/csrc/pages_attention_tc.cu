@@ -455,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-    } else if (warp == kWarpMma && lane == 0) {
+    } else if (warp == kWarpMma) {
+      const bool leader = elect_one();
       // ---- MMA issuer: one copy of each product's code, the chain a variable
       constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // 8-row groups, version, 128-byte swizzle
       auto desc = [](uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; };
@@ -467,14 +468,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0, nq = 0;
       bool ok = true;
       auto issue_pv = [&](int X, uint32_t pend) -> bool {
-        if (!mbar_wait(bar(B_PFULL0 + X), (X ? xt_b : xt_a) & 1u, p.st, 108)) return false;
+        if (!mbar_wait_warp(bar(B_PFULL0 + X), (X ? xt_b : xt_a) & 1u, p.st, 108)) return false;
         tc_fence_after();
         const uint32_t tS = tmem + 128 * X, tO = tmem + 256 + 128 * X;
         const uint32_t v = v_lo + (pend >> 8) * (NH * kHalf >> 4);
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? ~pend & 2u : 1u);
-        if (pend & 4u) tc_commit(bar(B_OFULL0 + X));
+          for (int k = 0; k < kKeys / 16; ++k)
+            tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? ~pend & 2u : 1u);
+          if (pend & 4u) tc_commit(bar(B_OFULL0 + X));
+        }
+        __syncwarp();
         if (X) ++xt_b; else ++xt_a;
         return true;
       };
@@ -483,10 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = walk.t1 - walk.t0;
         for (int lt = 0; lt < nt && ok; ++lt, ++n) {
           const uint32_t slot = n % SLOTS;
-          ok = mbar_wait(kvbar(KFULL, slot), n / SLOTS & 1u, p.st, 111);
+          ok = mbar_wait_warp(kvbar(KFULL, slot), n / SLOTS & 1u, p.st, 111);
           if (lt == 0)
             for (uint32_t b = nq; b < nq + (two ? 2 : 1) && ok; ++b)
-              ok = mbar_wait(bar(B_QFULL0 + (b & 1u)), b >> 1 & 1u, p.st, 110);
+              ok = mbar_wait_warp(bar(B_QFULL0 + (b & 1u)), b >> 1 & 1u, p.st, 110);
           if (!ok) break;
           const int subs = two || lt == 0 ? 2 : 1;
 #pragma unroll 1
@@ -501,13 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               const uint32_t qb = (nq + (two ? X : 0)) & 1u;
               const uint32_t q = q_lo + qb * (NH * kHalf >> 4), k0 = k_lo + slot * (NH * kHalf >> 4);
+              if (leader) {
 #pragma unroll
-              for (int k = 0; k < HD / 16; ++k) {
-                const uint32_t o = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
-                tc_mma_f16(tmem + 128 * X, desc(q + o), desc(k0 + o), kIdescS, k > 0 ? 1u : 0u);
+                for (int k = 0; k < HD / 16; ++k) {
+                  const uint32_t o = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+                  tc_mma_f16(tmem + 128 * X, desc(q + o), desc(k0 + o), kIdescS, k > 0 ? 1u : 0u);
+                }
+                tc_commit(bar(B_SFULL0 + X));
+                if (lt == nt - 1) tc_commit(bar(B_QEMPTY0 + qb));
               }
-              tc_commit(bar(B_SFULL0 + X));
-              if (lt == nt - 1) tc_commit(bar(B_QEMPTY0 + qb));
+              __syncwarp();
               const int step = two ? 1 : 2;
               pend = 1u | (lt < step ? 2u : 0u) | (lt + step >= nt ? 4u : 0u) | slot << 8;
             }
@@ -516,15 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
               pend_a = pend;
           }
-          if (ok) tc_commit(kvbar(STEP, slot));
+          if (ok && leader) tc_commit(kvbar(STEP, slot));
         }
         nq += two ? 2 : 1;
       }
       if (ok && pend_a) ok = issue_pv(0, pend_a);
       if (ok && pend_b) ok = issue_pv(1, pend_b);
       // no tensor-core operation of this CTA may outlive its TMEM
-      tc_commit(bar(B_DRAIN));
-      mbar_wait(bar(B_DRAIN), 0, p.st, 112);
+      if (leader) tc_commit(bar(B_DRAIN));
+      mbar_wait_warp(bar(B_DRAIN), 0, p.st, 112);
     }
   }
 
