@@ -150,8 +150,9 @@ inline PagesWork pages_work(void* ws, int64_t n_pages, int64_t n_seqs) {
 // ---- batch plan --------------------------------------------------------------
 // Which kernel reads the batch, decided by the host from sizes alone.
 enum PagesPath {
-  kPathSimt16,  // fp32, up to 16 (token, query head) rows per KV head
-  kPathSimt64,  // fp32
+  kPathSimt16,  // fp32 of other head_dim than 64 and 128, up to 16 (token, query head) rows per KV head
+  kPathSimt64,  // the same, more rows
+  kPathF32,     // fp32, tcgen05
   kPathFew,     // 16-bit, up to 16 rows per KV head: bound by reading K and V
   kPathTc       // 16-bit, tcgen05
 };
@@ -159,12 +160,13 @@ struct PathShape {
   int slots;       // (token, query head) rows of one sub-tile
   int subs;        // sub-tiles of one item
   int keys;        // keys of one tile
-  int grain;       // tiles of one unit in a batch too small to fill the CTAs for long (else 1)
+  int grain;       // tiles of one unit in a batch of up to `few` tiles per CTA (else 1)
+  int few;
   int ctas_per_sm;
   int part_words;  // fp32 words of one partial result: subs x slots x (head_dim + 2)
   int tokens(int group) const { return subs * (slots / group); }  // of one item
 };
-PagesPath pages_path(int dtype, int64_t max_rows, int group);
+PagesPath pages_path(int dtype, int head_dim, int64_t max_rows, int group);
 PathShape pages_path_shape(PagesPath path, int head_dim);
 
 // One piece of attention work: the query rows [row0, row0 + n_rows) of one
@@ -291,6 +293,8 @@ struct AttnArgs {
   float scale;
 };
 cudaError_t pages_attention_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool few, cudaStream_t s);
+// fp32 of head_dim 64 and 128 (pages_attention_f32.cu)
+cudaError_t pages_attention_f32(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s);
 // 16-bit elements (pages_attention_few.cu, pages_attention_tc.cu); n_rows: rows of q
 cudaError_t pages_attention_few(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, cudaStream_t s);
 cudaError_t pages_attention_tc(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, int n_rows,

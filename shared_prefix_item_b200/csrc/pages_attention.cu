@@ -1,5 +1,5 @@
-// Attention of a chunk of query rows over a paged KV cache: the fp32 path, on
-// CUDA cores (the tensor cores have no fp32 operands).
+// Attention of a chunk of query rows over a paged KV cache: fp32 elements of a
+// head_dim that the tensor-core kernel does not take, on CUDA cores.
 //
 // One pass over the keys with a running maximum and sum: for a tile of 64
 // keys, s = q.k scale (base 2), m' = max(m, max s), p = 2^(s - m'),
@@ -7,8 +7,13 @@
 // lse = ln 2 (m + log2 l).  Every statistic and O are fp32.
 //
 // An item's rows are (token, query head) slots of one KV head, so a K/V tile
-// is read once for all heads that share it; 256 threads hold a slots x 64
-// tile of scores (rows x 4 keys each) and slots x head_dim of O.
+// is read once for all heads that share it; 256 threads hold a slots x 64 tile
+// of scores (slots / 16 rows x 4 keys each) and slots x head_dim of O.  The
+// products run on packed fp32 pairs: of the scores' sums over even and odd
+// elements, of O two columns.  K of the next tile is fetched (cp.async) while
+// the softmax and P V run, V while the next scores do, so one buffer of each
+// is enough and no load is waited for.  Bound by shared-memory reads for chunks,
+// by latency for single tokens (16 slots, two CTAs per SM).
 #include "pages.cuh"
 
 namespace duolm {
@@ -18,16 +23,24 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTile = 64;
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until at most the last N groups of this thread are on the way
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 }  // namespace
 
-// M: slots of an item; NC: head_dim / 16, rounded up to what is instantiated
+// M: slots of an item; NC: head_dim / 32, rounded up to what is instantiated
 template <int M, int NC>
-__global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, PagesPlan pl, AttnArgs a) {
-  constexpr int RM = M / 16;
-  constexpr int E = 4;
-  extern __shared__ float smem[];
+__global__ void __launch_bounds__(kThreads, M == 16 && NC <= 4 ? 2 : 1)
+    attention_simt_kernel(PagesView p, PagesPlan pl, AttnArgs a) {
+  constexpr int RM = M / 16, LDP = kTile + 4;
+  extern __shared__ __align__(16) float smem[];
   __shared__ int s_last;
-  const int hd = p.head_dim, ld = hd + 4, nc = hd / 16, words = hd / E;
+  const int hd = p.head_dim, ld = hd + 4, nc = hd / 32, words = hd / 4;
   float* Qs = smem;
   float* Ks = Qs + M * ld;
   float* Vs = Ks + kTile * ld;
@@ -35,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
   pdl_launch_dependents();
   pdl_wait();
   if (!plan_usable(p, pl)) return;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, cta = blockIdx.x;
   const float scale2 = a.scale * 1.4426950408889634f;
   const int64_t layer_elems = p.layer_bytes() / 4, page_elems = p.page_bytes() / 4,
@@ -43,63 +56,88 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
   const float* kbase = reinterpret_cast<const float*>(p.k) + a.layer * layer_elems;
   const float* vbase = reinterpret_cast<const float*>(p.v) + a.layer * layer_elems;
   PageItem it;
+  // rows warp, warp + 8, .. of a tile of K or V; rows behind the last key are zeros
+  auto load_tile = [&](const float* base, float* dst, int dst_ld, int t) {
+    const int key_l = t * kTile + warp + 8 * (lane & 7);
+    int id_l = 0;
+    if (key_l < it.n_keys) {
+      id_l = p.table[(int64_t)it.seq * p.max_pages + (key_l >> p.page_shift)];
+      if ((unsigned)id_l >= (unsigned)p.n_pages) {
+        raise_on_plan(p, pl, ERR_BAD_INDEX, 90);
+        id_l = 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kTile / 8; ++j) {
+      const int r = warp + 8 * j, key = t * kTile + r;
+      const int id = __shfl_sync(0xffffffffu, id_l, j);
+      const bool have = key < it.n_keys;
+      const float* src = base + id * page_elems + it.kv_head * head_elems + (int64_t)(key & (p.page_tokens - 1)) * hd;
+      for (int c = lane; c < words; c += 32) cp_async16(smem_u32(dst + r * dst_ld + 4 * c), have ? src + 4 * c : base, have);
+    }
+    cp_commit();
+  };
   for (ItemWalk walk(pl, cta); walk.next(&it);) {
     const int t0 = walk.t0, t1 = walk.t1;
     __syncthreads();  // the previous item's shared tiles are done with
-    for (int i = tid; i < M * words; i += kThreads) {
-      const int r = i / words, c = i % words, j = r / G;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (j < it.n_rows)
-        x = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(a.q) + (int64_t)(it.row0 + j) * a.q_stride +
-                                            (int64_t)(it.kv_head * G + r % G) * hd + c * E);
-      *reinterpret_cast<uint4*>(Qs + r * ld + c * E) = x;
+    for (int r = warp; r < M; r += kThreads / 32) {
+      const int j = r / G;
+      const bool have = j < it.n_rows;
+      const float* src = reinterpret_cast<const float*>(a.q) + (int64_t)(it.row0 + j) * a.q_stride +
+                         (int64_t)(it.kv_head * G + r % G) * hd;
+      for (int c = lane; c < words; c += 32)
+        cp_async16(smem_u32(Qs + r * ld + 4 * c), have ? src + 4 * c : reinterpret_cast<const float*>(a.q), have);
     }
-    float m[RM], l[RM], acc[RM][NC];
+    load_tile(kbase, Ks, ld, t0);  // (Q is in its group)
+    load_tile(vbase, Vs, hd, t0);
+    float m[RM], l[RM];
+    float2 acc[RM][NC];
     int vis[RM];
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
-      const int j = (ty * RM + i) / G;
+      const int j = (ty + 16 * i) / G;
       vis[i] = a.causal ? min(max(it.last0 + j + 1, 0), it.n_keys) : it.n_keys;
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
+      for (int c = 0; c < NC; ++c) acc[i][c] = make_float2(0.f, 0.f);
     }
-    const int32_t* table = p.table + (int64_t)it.seq * p.max_pages;
     for (int t = t0; t < t1; ++t) {
       const int k0 = t * kTile;
+      cp_wait<1>();  // K of this tile
       __syncthreads();
-      for (int i = tid; i < kTile * words; i += kThreads) {
-        const int r = i / words, c = i % words, key = k0 + r;
-        uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-        if (key < it.n_keys) {
-          const int page = table[key >> p.page_shift];
-          if ((unsigned)page < (unsigned)p.n_pages) {
-            const int64_t at = page * page_elems + it.kv_head * head_elems +
-                               (int64_t)(key & (p.page_tokens - 1)) * hd + c * E;
-            kx = *reinterpret_cast<const uint4*>(kbase + at);
-            vx = *reinterpret_cast<const uint4*>(vbase + at);
-          } else {
-            raise_on_plan(p, pl, ERR_BAD_INDEX, 90);
+      float s[RM][4];
+      {
+        float2 s2[RM][4];
+#pragma unroll
+        for (int i = 0; i < RM; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 2
+        for (int d = 0; d < hd; d += 4) {
+          float4 kv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * ld + d);
+#pragma unroll
+          for (int i = 0; i < RM; ++i) {
+            const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * ld + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s2[i][j] = ffma2(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y), s2[i][j]);
+              s2[i][j] = ffma2(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), s2[i][j]);
+            }
           }
         }
-        *reinterpret_cast<uint4*>(Ks + r * ld + c * E) = kx;
-        *reinterpret_cast<uint4*>(Vs + r * hd + c * E) = vx;
+#pragma unroll
+        for (int i = 0; i < RM; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
       }
       __syncthreads();
-      float s[RM][4] = {};
-      for (int d = 0; d < hd; d += 4) {
-        float4 kv[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * ld + d);
-#pragma unroll
-        for (int i = 0; i < RM; ++i) {
-          const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty * RM + i) * ld + d);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s[i][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[i][j]))));
-        }
-      }
+      if (t + 1 < t1)
+        load_tile(kbase, Ks, ld, t + 1);
+      else
+        cp_commit();
 #pragma unroll
       for (int i = 0; i < RM; ++i) {
         float mx = m[i];
@@ -116,32 +154,45 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float pj = exp2f(s[i][j] - base);
-          Ps[(ty * RM + i) * (kTile + 4) + tx + 16 * j] = pj;
+          Ps[(ty + 16 * i) * LDP + tx + 16 * j] = pj;
           sum += pj;
         }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        l[i] = l[i] * corr + sum;
+        l[i] = l[i] * corr + sum;  // of this lane's keys
         m[i] = mx;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) acc[i][c] *= corr;
+        for (int c = 0; c < NC; ++c) acc[i][c] = fmul2(acc[i][c], make_float2(corr, corr));
       }
-      __syncwarp();  // a row's scores are written and read by one half-warp
-      for (int k = 0; k < kTile; k += 4) {
-        float4 pv[RM];
+      cp_wait<1>();     // V of this tile
+      __syncthreads();  // (a row's scores are written and read by one half-warp)
+#pragma unroll 2
+      for (int k = 0; k < kTile; k += 2) {
+        float2 v[2][NC];
 #pragma unroll
-        for (int i = 0; i < RM; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (ty * RM + i) * (kTile + 4) + k);
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          if (c >= nc) break;
-          const float* v = Vs + k * hd + tx + 16 * c;
+          for (int c = 0; c < NC; ++c)
+            if (c < nc) v[e][c] = *reinterpret_cast<const float2*>(Vs + (k + e) * hd + 2 * tx + 32 * c);
 #pragma unroll
-          for (int i = 0; i < RM; ++i)
-            acc[i][c] = fmaf(pv[i].x, v[0], fmaf(pv[i].y, v[hd], fmaf(pv[i].z, v[2 * hd], fmaf(pv[i].w, v[3 * hd], acc[i][c]))));
+        for (int i = 0; i < RM; ++i) {
+          const float2 pv = *reinterpret_cast<const float2*>(Ps + (ty + 16 * i) * LDP + k);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            if (c >= nc) break;
+            acc[i][c] = ffma2(make_float2(pv.x, pv.x), v[0][c], acc[i][c]);
+            acc[i][c] = ffma2(make_float2(pv.y, pv.y), v[1][c], acc[i][c]);
+          }
         }
       }
-      __syncwarp();
+      __syncthreads();
+      if (t + 1 < t1)
+        load_tile(vbase, Vs, hd, t + 1);
+      else
+        cp_commit();
     }
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
     if (!walk.whole(it)) {
       // divided among CTAs: the last to arrive joins the parts
       const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
@@ -151,11 +202,8 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
       for (int i = 0; i < RM; ++i) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-          if (c < nc) __stcg(mine + (i * nc + c) * kThreads + tid, acc[i][c]);
-        if (tx == 0) {
-          __stcg(mine + M * hd + ty * RM + i, m[i]);
-          __stcg(mine + M * hd + M + ty * RM + i, l[i]);
-        }
+          if (c < nc) __stcg(reinterpret_cast<float2*>(mine) + (i * nc + c) * kThreads + tid, acc[i][c]);
+        if (tx == 0) __stcg(reinterpret_cast<float2*>(mine + M * hd) + ty + 16 * i, make_float2(m[i], l[i]));
       }
       __threadfence();
       __syncthreads();
@@ -169,32 +217,34 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(PagesView p, P
       __threadfence();
 #pragma unroll
       for (int i = 0; i < RM; ++i) {
-        const int r = ty * RM + i;
+        const int r = ty + 16 * i;
+        auto stat = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(part_of(pl, part_words, c, c == c0) + M * hd) + r); };
         m[i] = -INFINITY;
-        for (int c = c0; c <= c1; ++c) m[i] = fmaxf(m[i], __ldcg(part_of(pl, part_words, c, c == c0) + M * hd + r));
+        for (int c = c0; c <= c1; ++c) m[i] = fmaxf(m[i], stat(c).x);
         const float base = m[i] == -INFINITY ? 0.f : m[i];
         l[i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < NC; ++k) acc[i][k] = 0.f;
+        for (int k = 0; k < NC; ++k) acc[i][k] = make_float2(0.f, 0.f);
         for (int c = c0; c <= c1; ++c) {
-          const float* part = part_of(pl, part_words, c, c == c0);
-          const float wt = exp2f(__ldcg(part + M * hd + r) - base);
-          l[i] = fmaf(wt, __ldcg(part + M * hd + M + r), l[i]);
+          const float2* part = reinterpret_cast<const float2*>(part_of(pl, part_words, c, c == c0));
+          const float2 st = stat(c);
+          const float wt = exp2f(st.x - base);
+          l[i] = fmaf(wt, st.y, l[i]);
 #pragma unroll
           for (int k = 0; k < NC; ++k)
-            if (k < nc) acc[i][k] = fmaf(wt, __ldcg(part + (i * nc + k) * kThreads + tid), acc[i][k]);
+            if (k < nc) acc[i][k] = ffma2(make_float2(wt, wt), __ldcg(part + (i * nc + k) * kThreads + tid), acc[i][k]);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
-      const int r = ty * RM + i, j = r / G, h = it.kv_head * G + r % G;
+      const int r = ty + 16 * i, j = r / G, h = it.kv_head * G + r % G;
       if (j >= it.n_rows) continue;
       const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : NAN);  // a row that sees no key gives zeros
       float* dst = reinterpret_cast<float*>(a.o) + (int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * hd;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (c < nc) dst[tx + 16 * c] = acc[i][c] * inv;
+        if (c < nc) *reinterpret_cast<float2*>(dst + 2 * tx + 32 * c) = fmul2(acc[i][c], make_float2(inv, inv));
       if (a.lse && tx == 0)
         a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m[i] == -INFINITY ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
     }
@@ -213,9 +263,9 @@ cudaError_t launch_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs&
 
 template <int M>
 cudaError_t simt_dim(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
-  if (p.head_dim <= 64) return launch_simt<M, 4>(p, pl, a, s);
-  if (p.head_dim <= 128) return launch_simt<M, 8>(p, pl, a, s);
-  return launch_simt<M, 16>(p, pl, a, s);
+  if (p.head_dim <= 64) return launch_simt<M, 2>(p, pl, a, s);
+  if (p.head_dim <= 128) return launch_simt<M, 4>(p, pl, a, s);
+  return launch_simt<M, 8>(p, pl, a, s);
 }
 
 }  // namespace

@@ -1,0 +1,475 @@
+// Attention of a chunk of query rows over a paged KV cache on 5th-generation
+// tensor cores, fp32 elements.
+//
+// The tensor cores have no fp32 operands, but every fp32 number is the sum of
+// three bf16 numbers that each take 8 of its 24 bits: x0 = x cut to 8 bits,
+// x1 = x - x0 cut to 8 bits, x2 = x - x0 - x1, all exact.  Of the nine products
+// of two such sums the six with i + j <= 2 are kept; the largest of the others
+// is below 2^-23 of the whole.  That is a sixth of the bf16 rate, 640
+// multiply-adds per cycle and SM, five times what the CUDA cores do.  Products
+// of bf16 numbers are exact; the tensor core's fp32 sums are cut, not rounded,
+// so a long sum drifts: the small products go first, the sum of a tile (4
+// steps of the large ones) starts anew, and the tiles are added up in rounded
+// fp32 by the softmax warps.  With all tiles summed in the tensor core the
+// output of 16 chunks over 1,000 tokens was off by 6.7e-6 of its size.
+//
+// The softmax is one pass with a running maximum, as in the 16-bit kernel.  An
+// item is 128 (token, query head) rows of one entry under one KV head, a tile
+// 64 keys.  One CTA per SM, 13 warps:
+//   warps 0-3   softmax: a thread holds a row (its TMEM lane) and 64 keys;
+//   warps 4-7   K: global memory to registers a tile ahead, cut in three,
+//               stored to shared memory in the 128-byte swizzle; half of Q;
+//   warps 8-11  V and the other half of Q, alike.  Rows behind the last key are
+//               stored as zeros: the slots may hold anything;
+//   warp 12     tcgen05.mma: S(t + 1) before P V of t, so that the tensor core
+//               works on S(t + 1) while the softmax of t runs.
+// The tensor core is the bound: 48 products of 48 cycles and 24 of 64 for a
+// tile of head_dim 128.  K is stored while P V runs, V while S does, so one
+// buffer of each is enough.  Tensor memory: two buffers (even and odd tiles) of
+// 96 columns, S in the first 64 and then the three parts of P over them; from
+// 192 T = P V of one tile, from 320 O.
+#include "kernels.cuh"
+#include "pages.cuh"
+
+namespace duolm {
+
+namespace {
+
+constexpr int kSlots = 128, kKeys = 64;
+constexpr int kThreads = 13 * 32, kWarpMma = 12;
+constexpr uint32_t kTmemCols = 512, kColBuf = 96, kColT = 192, kColO = 320;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int HD>
+struct Lay {
+  static constexpr int NH = HD / 64;
+  static constexpr int QHALF = kSlots * 128, KHALF = kKeys * 128;          // 64 elements of every row
+  static constexpr int QPART = NH * QHALF, KPART = NH * KHALF;             // one of the three parts
+  static constexpr int Q = 0, K = 3 * QPART, V = K + 3 * KPART, BAR = V + 3 * KPART;
+  static constexpr int SMEM = BAR + 128 + 1024;
+};
+
+enum { B_QFULL, B_KFULL, B_VFULL, B_SFULL0, B_SFULL1, B_PFULL0, B_PFULL1, B_PV, B_TFREE, B_DRAIN, B_COUNT };
+
+// the largest part of x that bf16 holds, towards zero
+__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// two cut values as bf16, a in the low half
+__device__ __forceinline__ uint32_t pack_cut(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
+// Eight floats to the three parts' 16-byte words.
+__device__ __forceinline__ void split8(const float4& a, const float4& b, uint4 (&w)[3]) {
+  float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = pack_cut(x[2 * i], x[2 * i + 1]);
+      if (k < 2) {
+        x[2 * i] -= cut(x[2 * i]);
+        x[2 * i + 1] -= cut(x[2 * i + 1]);
+      }
+    }
+    w[k] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+__device__ __forceinline__ void join_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+}  // namespace
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesView p, PagesPlan pl, AttnArgs a) {
+  using L = Lay<HD>;
+  constexpr int NH = L::NH, CPR = HD / 8;  // 8-element words of a row
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kSlots, kKeys);
+  constexpr uint32_t kIdescPV = idesc_bf16_f32(kSlots, HD) | (1u << 16);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + B_COUNT);
+  int* s_last = reinterpret_cast<int*>(tmem_holder + 1);
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B_COUNT; ++i)
+      mbar_init(bar(i), i == B_QFULL ? 8u : i == B_KFULL || i == B_VFULL || i == B_PFULL0 || i == B_PFULL1 || i == B_TFREE ? 4u : 1u);
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  const bool usable = plan_usable(p, pl);
+  const int cta = blockIdx.x, G = a.group;
+  PageItem it;
+
+  // Every role walks the same items and tiles; n counts the CTA's tiles.
+  if (!usable) {
+    // straight to the teardown
+  } else if (warp < 4) {
+    const int r = threadIdx.x;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t tT = tmem + lane_off + kColT, tO = tmem + lane_off + kColO;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    uint32_t n = 0;
+    bool ok = true;
+    for (ItemWalk walk(pl, cta); walk.next(&it);) {
+      const int j = r / G;
+      const bool valid = j < it.n_rows && r < kSlots / G * G;
+      const bool live = __any_sync(0xffffffffu, valid);
+      const int vis = a.causal ? min(max(it.last0 + j + 1, 0), it.n_keys) : it.n_keys;
+      float m_used = -INFINITY, l = 0.f;
+      float corr_t = 0.f;  // what O up to the tile before T's is to be multiplied by; 0: there is none
+      for (int t = walk.t0; t < walk.t1; ++t, ++n) {
+        const uint32_t b = n & 1u, tS = tmem + lane_off + kColBuf * b;
+        ok = ok && mbar_wait_warp(bar(B_SFULL0 + b), n >> 1 & 1u, p.st, 130);
+        float corr = 1.f;
+        if (ok && live) {
+          tc_fence_after();
+          uint32_t sr[2][32];
+          tmem_ld32_async(tS, sr[0]);
+          tmem_ld32_async(tS + 32, sr[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) tmem_ld_fence(sr[c][i]);
+          const int n_vis = vis - t * kKeys;  // of this tile
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              if (32 * c + i >= n_vis) sr[c][i] = __float_as_uint(-INFINITY);
+              if (32 * c + i + 1 >= n_vis) sr[c][i + 1] = __float_as_uint(-INFINITY);
+              mx = fmax3f(mx, __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+            }
+          const float m_new = fmaxf(m_used, mx * scale_log2);
+          if (t == walk.t0) {
+            m_used = m_new;
+          } else if (m_new > m_used + kRescaleLog2) {
+            corr = fast_exp2(m_used - m_new);
+            l *= corr;
+            m_used = m_new;
+          }
+          const float nmu = m_used == -INFINITY ? 0.f : -m_used;  // no key of this row yet
+          float ls[2] = {0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[3][16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float e0 = fast_exp2(fmaf(__uint_as_float(sr[c][2 * i]), scale_log2, nmu));
+              float e1 = fast_exp2(fmaf(__uint_as_float(sr[c][2 * i + 1]), scale_log2, nmu));
+              ls[0] += e0;
+              ls[1] += e1;
+#pragma unroll
+              for (int k = 0; k < 3; ++k) {
+                pk[k][i] = pack_cut(e0, e1);
+                e0 -= cut(e0);
+                e1 -= cut(e1);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) tmem_st16_async(tS + 32 * k + 16 * c, pk[k]);
+          }
+          l += ls[0] + ls[1];
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL0 + b));
+        if (t > walk.t0) {
+          // O = O corr + T of the last tile, while this tile's P V waits for T
+          ok = ok && mbar_wait_warp(bar(B_PV), (n - 1) & 1u, p.st, 131);
+          if (ok && live) {
+            tc_fence_after();
+            const bool has_o = t > walk.t0 + 1;
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+              uint32_t tv[32], ov[32];
+              tmem_ld32_async(tT + 32 * c, tv);
+              if (has_o) tmem_ld32_async(tO + 32 * c, ov);
+              tmem_wait_ld();
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                tmem_ld_fence(tv[i]);
+                tmem_ld_fence(ov[i]);
+                v[i] = __uint_as_float(tv[i]);
+                if (has_o) v[i] = fmaf(__uint_as_float(ov[i]), corr_t, v[i]);
+              }
+              tmem_st32(tO + 32 * c, v);
+            }
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_TFREE));
+        }
+        corr_t = corr;
+      }
+      // ---- the item's end: T of the last tile
+      ok = ok && mbar_wait_warp(bar(B_PV), (n - 1) & 1u, p.st, 132);
+      tc_fence_after();
+      const bool has_o = walk.t1 - walk.t0 > 1;
+      const bool whole = walk.whole(it), act = live && ok;
+      const int h = it.kv_head * G + r % G;
+      float* dst = reinterpret_cast<float*>(a.o) + (int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD;
+      const int64_t at_lse = (int64_t)(it.row0 + j) * a.n_q_heads + h;
+      constexpr int kPart = kSlots * (HD + 2);
+      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
+      float* part = part_of(pl, kPart, cta, cta == c0);
+      if (act) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a row that sees no key gives zeros
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          float v[32];
+          tmem_ld32(tT + 32 * c, v);
+          if (has_o) {
+            float o[32];
+            tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(o[i], corr_t, v[i]);
+          }
+          if (!valid) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (whole)
+              reinterpret_cast<float4*>(dst)[8 * c + i] =
+                  make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+            else
+              __stcg(reinterpret_cast<float4*>(part) + (8 * c + i) * kSlots + r,
+                     make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
+        }
+        tc_fence_before();
+        if (valid && !whole) __stcg(reinterpret_cast<float2*>(part + kSlots * HD) + r, make_float2(m_used, l));
+        if (valid && whole && a.lse) a.lse[at_lse] = m_used == -INFINITY ? -INFINITY : m_used * kLn2 + logf(l);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_TFREE));
+      if (whole) continue;
+      // ---- divided among CTAs: the last to arrive joins the parts, in CTA order
+      __threadfence();
+      join_sync();
+      if (threadIdx.x == 0) {
+        const int k = atomicAdd(&pl.arrived[walk.index], 1);
+        *s_last = k == c1 - c0;
+        if (*s_last) pl.arrived[walk.index] = 0;
+      }
+      join_sync();
+      if (!*s_last || !act || !valid) continue;
+      __threadfence();
+      auto stat = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(part_of(pl, kPart, c, c == c0) + kSlots * HD) + r); };
+      float m = -INFINITY;
+      for (int c = c0; c <= c1; ++c) m = fmaxf(m, stat(c).x);
+      const float base = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float2 s = stat(c);
+        l = fmaf(s.y, fast_exp2(s.x - base), l);
+      }
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+      for (int k = 0; k < HD / 16; ++k) {
+        float4 acc[4] = {};
+        for (int c = c0; c <= c1; ++c) {
+          const float w = fast_exp2(stat(c).x - base);
+          const float* pc = part_of(pl, kPart, c, c == c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pc) + (4 * k + i) * kSlots + r);
+            acc[i].x = fmaf(w, v.x, acc[i].x), acc[i].y = fmaf(w, v.y, acc[i].y);
+            acc[i].z = fmaf(w, v.z, acc[i].z), acc[i].w = fmaf(w, v.w, acc[i].w);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<float4*>(dst)[4 * k + i] =
+              make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+      }
+      if (a.lse) a.lse[at_lse] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+    }
+    if (!ok && lane == 0) pl.head->stale = 1;
+  } else if (warp < kWarpMma) {
+    // ---- K (warps 4-7) or V (8-11), and half of Q each
+    const bool is_v = warp >= 8;
+    const int tid = threadIdx.x & 127;
+    const char* pool = (is_v ? p.v : p.k) + a.layer * p.layer_bytes();
+    // word c of row `row` of a part whose 64-element halves are `half_bytes` apart
+    auto place = [&](uint32_t base, int half_bytes, int row, int c) {
+      return base + (c >> 3) * half_bytes + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    };
+    auto store3 = [&](uint32_t at, int part_bytes, const float4& x, const float4& y) {
+      uint4 w[3];
+      split8(x, y, w);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(smem + at + k * part_bytes) = w[k];
+    };
+    constexpr int WORDS = kKeys * CPR / 128;  // 8-element words of a tile per thread
+    float4 buf[2 * WORDS];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) {
+        const int e = tid + 128 * i, row = e / CPR, c = e % CPR, key = t * kKeys + row;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (key < it.n_keys) {
+          const int id = p.table[(int64_t)it.seq * p.max_pages + (key >> p.page_shift)];
+          if ((unsigned)id < (unsigned)p.n_pages) {
+            const float4* src = reinterpret_cast<const float4*>(pool + id * p.page_bytes() + it.kv_head * p.head_bytes() +
+                                                               (int64_t)(key & (p.page_tokens - 1)) * (HD * 4)) + 2 * c;
+            x = __ldcg(src);
+            y = __ldcg(src + 1);
+          } else {
+            raise_on_plan(p, pl, ERR_BAD_INDEX, 133);
+          }
+        }
+        buf[2 * i] = x;
+        buf[2 * i + 1] = y;
+      }
+    };
+    ItemWalk walk(pl, cta);
+    bool have = walk.next(&it), first = true, ok = true;
+    int t = walk.t0;
+    if (have) fetch(t);
+    for (uint32_t n = 0; have && ok; ++n) {
+      if (first) {
+        // Q: the S that read the last item's has to be over
+        if (n > 0 && !(ok = mbar_wait_warp(bar(B_SFULL0 + ((n - 1) & 1u)), (n - 1) >> 1 & 1u, p.st, 134))) break;
+        constexpr int QW = kSlots / 2 * CPR / 128;  // words per thread
+#pragma unroll 1
+        for (int i0 = 0; i0 < QW; i0 += QW / 4) {
+          float4 q[QW / 2];
+#pragma unroll
+          for (int i = 0; i < QW / 4; ++i) {
+            const int e = tid + 128 * (i0 + i), row = (is_v ? kSlots / 2 : 0) + e / CPR, c = e % CPR, j = row / G;
+            q[2 * i] = q[2 * i + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < it.n_rows && row < kSlots / G * G) {
+              const float4* src = reinterpret_cast<const float4*>(
+                  reinterpret_cast<const float*>(a.q) + (int64_t)(it.row0 + j) * a.q_stride +
+                  (int64_t)(it.kv_head * G + row % G) * HD) + 2 * c;
+              q[2 * i] = src[0];
+              q[2 * i + 1] = src[1];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < QW / 4; ++i) {
+            const int e = tid + 128 * (i0 + i), row = (is_v ? kSlots / 2 : 0) + e / CPR, c = e % CPR;
+            store3(place(L::Q, L::QHALF, row, c), L::QPART, q[2 * i], q[2 * i + 1]);
+          }
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_QFULL));
+        first = false;
+      }
+      // the product that read the last tile has to be over
+      if (n > 0) {
+        ok = is_v ? mbar_wait_warp(bar(B_PV), (n - 1) & 1u, p.st, 135)
+                  : mbar_wait_warp(bar(B_SFULL0 + ((n - 1) & 1u)), (n - 1) >> 1 & 1u, p.st, 136);
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) {
+        const int e = tid + 128 * i, row = e / CPR, c = e % CPR;
+        store3(place(is_v ? L::V : L::K, L::KHALF, row, c), L::KPART, buf[2 * i], buf[2 * i + 1]);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(is_v ? B_VFULL : B_KFULL));
+      if (++t >= walk.t1) {
+        have = walk.next(&it);
+        t = walk.t0;
+        first = true;
+      }
+      if (have) fetch(t);
+    }
+  } else {
+    // ---- MMA issuer
+    const bool leader = elect_one();
+    constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // 8-row groups, version, 128-byte swizzle
+    auto desc = [](uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; };
+    const uint32_t q_lo = ((sbase + L::Q) >> 4) | 1u << 16, k_lo = ((sbase + L::K) >> 4) | 1u << 16,
+                   v_lo = ((sbase + L::V) >> 4) | (uint32_t)(L::KHALF >> 4) << 16;
+    uint32_t n = 0, n_it = 0;
+    bool ok = true;
+    // the kept products, the small ones first
+    constexpr int kI[6] = {0, 1, 2, 0, 1, 0}, kJ[6] = {2, 1, 0, 1, 0, 0};
+    auto issue_pv = [&](uint32_t m) -> bool {  // of tile m
+      const uint32_t b = m & 1u;
+      if (!mbar_wait_warp(bar(B_PFULL0 + b), m >> 1 & 1u, p.st, 137)) return false;
+      if (!mbar_wait_warp(bar(B_VFULL), m & 1u, p.st, 138)) return false;
+      if (m > 0 && !mbar_wait_warp(bar(B_TFREE), (m - 1) & 1u, p.st, 142)) return false;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll
+        for (int x = 0; x < 6; ++x)
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            tc_mma_f16_ts(tmem + kColT, tmem + kColBuf * b + 32 * kI[x] + 8 * k,
+                          desc(v_lo + kJ[x] * (L::KPART >> 4) + k * 128), kIdescPV, x == 0 && k == 0 ? 0u : 1u);
+        tc_commit(bar(B_PV));
+      }
+      __syncwarp();
+      return true;
+    };
+    for (ItemWalk walk(pl, cta); ok && walk.next(&it); ++n_it) {
+      if (!(ok = mbar_wait_warp(bar(B_QFULL), n_it & 1u, p.st, 139))) break;
+      for (int t = walk.t0; t < walk.t1; ++t, ++n) {
+        if (!(ok = mbar_wait_warp(bar(B_KFULL), n & 1u, p.st, 140))) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int x = 0; x < 6; ++x)
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              tc_mma_f16(tmem + kColBuf * (n & 1u), desc(q_lo + (kI[x] * L::QPART + (k >> 2) * L::QHALF + (k & 3) * 32) / 16),
+                         desc(k_lo + (kJ[x] * L::KPART + (k >> 2) * L::KHALF + (k & 3) * 32) / 16), kIdescS,
+                         x == 0 && k == 0 ? 0u : 1u);
+          tc_commit(bar(B_SFULL0 + (n & 1u)));
+        }
+        __syncwarp();
+        if (t > walk.t0 && !(ok = issue_pv(n - 1))) break;
+      }
+      if (ok) ok = issue_pv(n - 1);
+    }
+    // no tensor-core operation of this CTA may outlive its TMEM
+    if (leader) tc_commit(bar(B_DRAIN));
+    mbar_wait_warp(bar(B_DRAIN), 0, p.st, 141);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+namespace {
+
+template <int HD>
+cudaError_t launch_f32(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(pages_attention_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Lay<HD>::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_ex(pages_attention_f32_kernel<HD>, dim3(pl.ctas), dim3(kThreads), Lay<HD>::SMEM, s, true, p, pl, a);
+}
+
+}  // namespace
+
+cudaError_t pages_attention_f32(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
+  return p.head_dim == 128 ? launch_f32<128>(p, pl, a, s) : launch_f32<64>(p, pl, a, s);
+}
+
+}  // namespace duolm

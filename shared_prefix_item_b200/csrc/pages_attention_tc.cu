@@ -13,8 +13,8 @@
 //   more than 128 rows: A and B are the two sub-tiles, and every K/V tile
 //     serves both;
 //   128 rows or fewer: both chains hold the same rows, A takes the even key
-//     tiles and B the odd ones, and A joins the two at the end (both O are in
-//     the same TMEM lanes, so no data but m and l crosses warps).
+//     tiles and B the odd ones, and at the end each joins half of the columns
+//     (both O are in the same TMEM lanes, so no data but m and l crosses warps).
 // One CTA per SM, 384 threads:
 //   warps 0-3 softmax of A, 4-7 of B: a thread holds a row (its TMEM lane) and
 //             128 keys;
@@ -63,8 +63,8 @@ struct Lay {
   static constexpr int NH = HD / 64;
   static constexpr int SLOTS = HD == 64 ? 4 : 2;  // K and V tiles in flight: 64 KB each
   static constexpr int Q = 0, K = Q + 2 * NH * kHalf, V = K + SLOTS * NH * kHalf, BAR = V + SLOTS * NH * kHalf;
-  static constexpr int STAT = BAR + 256;  // float2 [128]: m and l of chain B
-  static constexpr int SMEM = STAT + 1024 + 1024;
+  static constexpr int STAT = BAR + 256;  // float2 [2][128]: m and l of the chains
+  static constexpr int SMEM = STAT + 2048 + 1024;
 };
 
 enum { B_QFULL0, B_QFULL1, B_QEMPTY0, B_QEMPTY1, B_SFULL0, B_SFULL1, B_PFULL0, B_PFULL1, B_OFULL0, B_OFULL1, B_DRAIN, B_KV };
@@ -224,38 +224,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_xi;
         tc_fence_after();
       }
-      const bool joined = !two && nt > 1;  // A takes over B's half of the keys
-      const bool writes = two || X == 0;
+      // one set of rows, keys in both chains: each takes half of the columns
+      const bool joined = !two && nt > 1;
+      const bool writes = joined || two || X == 0;
       float wa = 1.f, wb = 0.f;
       if (joined) {
-        if (X == 1) stat[r] = make_float2(m_used, l);
-        named_sync(1);
-        if (X == 0) {
-          const float2 sb = stat[r];
-          const float m = fmaxf(m_used, sb.x), base = m == -INFINITY ? 0.f : m;
-          wa = fast_exp2(m_used - base);
-          wb = fast_exp2(sb.x - base);
-          l = l * wa + sb.y * wb;
-          m_used = m;
-        }
+        stat[X * kSub + r] = make_float2(m_used, l);
+        tc_fence_before();
+        named_sync(1);  // (both O are complete, too)
+        tc_fence_after();
+        const float2 sa = stat[r], sb = stat[kSub + r];
+        const float m = fmaxf(sa.x, sb.x), base = m == -INFINITY ? 0.f : m;
+        wa = fast_exp2(sa.x - base);
+        wb = fast_exp2(sb.x - base);
+        l = sa.y * wa + sb.y * wb;
+        m_used = m;
       }
       const bool whole = walk.whole(it);
       const int h = it.kv_head * G + r % G;
       const bool act = writes && live && ok;
+      const bool states = valid && (!joined || X == 0);  // writes the row's statistics
       float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a row that sees no key gives zeros
       char* dst = a.o + ((int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD) * 2;
       const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
       constexpr int kPart = 2 * kSub * (HD + 2), kRows = 2 * kSub;
       const int slot = (two ? X * kSub : 0) + r;
       float* part = part_of(pl, kPart, cta, cta == c0);
+      const int col0 = joined && X == 1 ? HD / 64 : 0, col1 = joined && X == 0 ? HD / 64 : HD / 32;  // of 32
+      const uint32_t tOA = joined ? tmem + lane_off + 256 : tO;
       if (act) {
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
+        for (int c = col0; c < col1; ++c) {
           uint32_t ov[32];
-          tmem_ld32_async(tO + 32 * c, ov);
+          tmem_ld32_async(tOA + 32 * c, ov);
           if (joined) {
             uint32_t ob[32];
-            tmem_ld32_async(tO + 128 + 32 * c, ob);
+            tmem_ld32_async(tOA + 128 + 32 * c, ob);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -287,11 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
-        if (valid && !whole) __stcg(reinterpret_cast<float2*>(part + kRows * HD) + slot, make_float2(m_used, l));
-        if (valid && whole && a.lse)
+        if (states && !whole) __stcg(reinterpret_cast<float2*>(part + kRows * HD) + slot, make_float2(m_used, l));
+        if (states && whole && a.lse)
           a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m_used == -INFINITY ? -INFINITY : (m_used + log2f(l)) * kLn2;
       }
-      if (joined) named_sync(2);  // A has read O of B
+      if (joined) named_sync(2);  // each has read the other's O and statistics
       if (whole) continue;
       // ---- divided among CTAs: the last to arrive joins the parts, in CTA order
       __threadfence();
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll 1
-      for (int k = 0; k < HD / 16; ++k) {
+      for (int k = 2 * col0; k < 2 * col1; ++k) {
         float4 acc[4] = {};
         for (int c = c0; c <= c1; ++c) {
           const float* pc = part_of(pl, kPart, c, c == c0);
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
         d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
-      if (a.lse)
+      if (states && a.lse)
         a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
     }
     if (!ok && lane == 0) pl.head->stale = 1;
@@ -492,16 +496,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t b = nq; b < nq + (two ? 2 : 1) && ok; ++b)
               ok = mbar_wait_warp(bar(B_QFULL0 + (b & 1u)), b >> 1 & 1u, p.st, 110);
           if (!ok) break;
-          const int subs = two || lt == 0 ? 2 : 1;
+          const int x0 = two ? 0 : lt & 1, x1 = two ? 2 : x0 + 1;
 #pragma unroll 1
-          for (int i = 0; i < subs; ++i) {
-            const int X = subs == 2 ? i : lt & 1;
+          for (int X = x0; X < x1; ++X) {
             uint32_t pend = X ? pend_b : pend_a;
-            if (pend) {
-              if (!(ok = issue_pv(X, pend))) break;
-              pend = 0;
-            }
-            if (two || i == 0) {  // (else: what the last item left of the other chain)
+            if (pend && !(ok = issue_pv(X, pend))) break;
+            {
               tc_fence_after();
               const uint32_t qb = (nq + (two ? X : 0)) & 1u;
               const uint32_t q = q_lo + qb * (NH * kHalf >> 4), k0 = k_lo + slot * (NH * kHalf >> 4);
@@ -526,9 +526,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && leader) tc_commit(kvbar(STEP, slot));
         }
         nq += two ? 2 : 1;
+        // the item's last P V, before anything waits for the next item's K
+        if (ok && pend_a) ok = issue_pv(0, pend_a);
+        if (ok && pend_b) ok = issue_pv(1, pend_b);
+        pend_a = pend_b = 0;
       }
-      if (ok && pend_a) ok = issue_pv(0, pend_a);
-      if (ok && pend_b) ok = issue_pv(1, pend_b);
       // no tensor-core operation of this CTA may outlive its TMEM
       if (leader) tc_commit(bar(B_DRAIN));
       mbar_wait_warp(bar(B_DRAIN), 0, p.st, 112);

@@ -6,19 +6,25 @@
 
 namespace duolm {
 
-PagesPath pages_path(int dtype, int64_t max_rows, int group) {
-  const bool few = std::max<int64_t>(max_rows, 1) * group <= 16;
-  if (dtype == DUOLM_DTYPE_FP32) return few ? kPathSimt16 : kPathSimt64;
-  return few ? kPathFew : kPathTc;
+PagesPath pages_path(int dtype, int head_dim, int64_t max_rows, int group) {
+  const int64_t slots = std::max<int64_t>(max_rows, 1) * group;
+  if (dtype != DUOLM_DTYPE_FP32) return slots <= 16 ? kPathFew : kPathTc;
+  if (head_dim == 64 || head_dim == 128) return kPathF32;
+  return slots <= 16 ? kPathSimt16 : kPathSimt64;
 }
 
 PathShape pages_path_shape(PagesPath path, int head_dim) {
   PathShape sh{};
-  sh.slots = path == kPathSimt64 ? 64 : path == kPathTc ? 128 : 16;
+  sh.slots = path == kPathSimt64 ? 64 : path == kPathTc || path == kPathF32 ? 128 : 16;
   sh.subs = path == kPathTc ? 2 : 1;
   sh.keys = path == kPathTc ? 128 : 64;
+  // Joining an item that was divided costs about as much as 8 tiles of a few
+  // rows (64 KB or less each) or 2 of a chunk; units of several tiles leave
+  // fewer items divided, and less even work.  36 rows each of 64 sequences of
+  // 404 tokens (14 tiles per CTA): 59 us with units of one tile, 52 with 4.
   sh.grain = path == kPathTc ? 4 : 8;
-  sh.ctas_per_sm = path == kPathFew ? 2 : 1;
+  sh.few = path == kPathTc ? 32 : 8;
+  sh.ctas_per_sm = path == kPathFew || (path == kPathSimt16 && head_dim <= 128) ? 2 : 1;
   sh.part_words = sh.subs * sh.slots * (head_dim + 2);
   return sh;
 }
@@ -95,7 +101,7 @@ __device__ __forceinline__ int key_tiles(int n_keys, int keys) { return max(1, (
 // sums in memory.  A chain of dependent loads bounds it: one CTA making the
 // items of 64 entries, a warp to an entry, took 24 us.
 __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, BatchView b, PagesPlan pl, int m,
-                                                                  int keys, int grain) {
+                                                                  int keys, int grain, int few) {
   extern __shared__ uint32_t seen[];
   __shared__ int s_scan[3][32];
   __shared__ uint32_t s_err;
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   __syncthreads();
   // A batch of few tiles is divided in units of several: a CTA then takes
   // longer over them, but fewer items are divided and joined.
-  const bool coarse = units[0] <= pl.ctas * grain;
+  const bool coarse = units[0] <= pl.ctas * few;
   const int total = coarse ? units[1] : units[0], ctas = min(pl.ctas, total);
   if (!coarse) grain = 1;
   const bool refused = s_err || units[0] >= kScanCap || items > pl.max_items;
@@ -441,7 +447,7 @@ int batch_layout(const duolm_pages* pages, const PagesView& p, const duolm_pages
   *sms = pages_sms(pages->device);
   if (!*sms) return pages_fail(DUOLM_E_CUDA, "device %d", pages->device);
   const int group = b->n_q_heads / p.n_kv_heads;
-  *path = pages_path(pages->dtype, b->max_rows, group);
+  *path = pages_path(pages->dtype, p.head_dim, b->max_rows, group);
   const PathShape sh = pages_path_shape(*path, p.head_dim);
   const int64_t need = pages_plan_layout(static_cast<char*>(b->plan), b->n, b->n_rows, p.n_kv_heads, group,
                                          sh, *sms * sh.ctas_per_sm, pl);
@@ -475,7 +481,7 @@ extern "C" int64_t duolm_pages_plan_bytes(const duolm_pages* pages, int n, int n
   const int sms = pages_sms(pages->device);
   if (!sms) return pages_fail(DUOLM_E_CUDA, "pages_plan_bytes: device %d", pages->device);
   const int group = n_q_heads / p.n_kv_heads;
-  const PathShape sh = pages_path_shape(pages_path(pages->dtype, max_rows, group), p.head_dim);
+  const PathShape sh = pages_path_shape(pages_path(pages->dtype, p.head_dim, max_rows, group), p.head_dim);
   const int64_t need = pages_plan_layout(nullptr, n, n_rows, p.n_kv_heads, group, sh, sms * sh.ctas_per_sm, nullptr);
   return need < 0 ? pages_fail(DUOLM_E_CAPACITY, "pages_plan_bytes: too many items") : need;
 }
@@ -501,7 +507,7 @@ extern "C" int duolm_pages_plan(const duolm_pages* pages, const duolm_pages_batc
     e = cudaFuncSetAttribute(batch_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
   if (e == cudaSuccess)
     e = launch_ex(batch_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(cuda_stream), true,
-                  p, b, pl, sh.tokens(group), sh.keys, sh.grain);
+                  p, b, pl, sh.tokens(group), sh.keys, sh.grain, sh.few);
   return e == cudaSuccess ? 0 : pages_fail(DUOLM_E_CUDA, "pages_plan: %s", cudaGetErrorString(e));
 }
 
@@ -584,6 +590,8 @@ extern "C" int duolm_pages_attention(const duolm_pages* pages, const duolm_pages
     e = pages_attention_few(p, pl, a, bf16, s);
   else if (path == kPathTc)
     e = pages_attention_tc(p, pl, a, bf16, batch->n_rows, s);
+  else if (path == kPathF32)
+    e = pages_attention_f32(p, pl, a, s);
   else
     e = pages_attention_simt(p, pl, a, path == kPathSimt16, s);
   return e == cudaSuccess ? 0 : pages_fail(DUOLM_E_CUDA, "pages_attention: %s", cudaGetErrorString(e));
