@@ -15,14 +15,15 @@
 //
 // The softmax is one pass with a running maximum, as in the 16-bit kernel.  An
 // item is 128 (token, query head) rows of one entry under one KV head, a tile
-// 64 keys.  One CTA per SM, 13 warps:
+// 64 keys.  One CTA per SM, 16 warps:
 //   warps 0-3   softmax: a thread holds a row (its TMEM lane) and 64 keys;
 //   warps 4-7   K: global memory to registers a tile ahead, cut in three,
 //               stored to shared memory in the 128-byte swizzle; half of Q;
 //   warps 8-11  V and the other half of Q, alike.  Rows behind the last key are
 //               stored as zeros: the slots may hold anything;
 //   warp 12     tcgen05.mma: S(t + 1) before P V of t, so that the tensor core
-//               works on S(t + 1) while the softmax of t runs.
+//               works on S(t + 1) while the softmax of t runs;
+//   warps 13-15 idle.
 // The tensor core is the bound: 48 products of 48 cycles and 24 of 64 for a
 // tile of head_dim 128.  K is stored while P V runs, V while S does, so one
 // buffer of each is enough.  Tensor memory: two buffers (even and odd tiles) of
@@ -36,7 +37,10 @@ namespace duolm {
 namespace {
 
 constexpr int kSlots = 128, kKeys = 64;
-constexpr int kThreads = 13 * 32, kWarpMma = 12;
+constexpr int kThreads = 512, kWarpMma = 12;
+// registers move from the last warpgroup to the others (sum: the launch's 512 x 128)
+constexpr int kRegLaunch = 128, kRegSoftmax = 168, kRegLoad = 144, kRegMma = 56;
+static_assert(kRegSoftmax + 2 * kRegLoad + kRegMma <= 4 * kRegLaunch, "register split above the launch's registers");
 constexpr uint32_t kTmemCols = 512, kColBuf = 96, kColT = 192, kColO = 320;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -119,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
   if (!usable) {
     // straight to the teardown
   } else if (warp < 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
     const int r = threadIdx.x;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t tT = tmem + lane_off + kColT, tO = tmem + lane_off + kColO;
@@ -147,16 +152,20 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
 #pragma unroll
             for (int i = 0; i < 32; ++i) tmem_ld_fence(sr[c][i]);
           const int n_vis = vis - t * kKeys;  // of this tile
-          float mx = -INFINITY;
+          if (__any_sync(0xffffffffu, n_vis < kKeys)) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i >= n_vis) sr[c][i] = __float_as_uint(-INFINITY);
+          }
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              if (32 * c + i >= n_vis) sr[c][i] = __float_as_uint(-INFINITY);
-              if (32 * c + i + 1 >= n_vis) sr[c][i + 1] = __float_as_uint(-INFINITY);
-              mx = fmax3f(mx, __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
-            }
-          const float m_new = fmaxf(m_used, mx * scale_log2);
+            for (int i = 0; i < 32; i += 2)
+              mx[c] = fmax3f(mx[c], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+          const float m_new = fmaxf(m_used, fmaxf(mx[0], mx[1]) * scale_log2);
           if (t == walk.t0) {
             m_used = m_new;
           } else if (m_new > m_used + kRescaleLog2) {
@@ -165,27 +174,27 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
             m_used = m_new;
           }
           const float nmu = m_used == -INFINITY ? 0.f : -m_used;  // no key of this row yet
-          float ls[2] = {0.f, 0.f};
+          const float2 sv = make_float2(scale_log2, scale_log2), nv = make_float2(nmu, nmu);
+          float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[3][16];
+          for (int c = 0; c < 4; ++c) {  // 16 keys at a time
+            uint32_t pk[3][8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float e0 = fast_exp2(fmaf(__uint_as_float(sr[c][2 * i]), scale_log2, nmu));
-              float e1 = fast_exp2(fmaf(__uint_as_float(sr[c][2 * i + 1]), scale_log2, nmu));
-              ls[0] += e0;
-              ls[1] += e1;
-#pragma unroll
-              for (int k = 0; k < 3; ++k) {
-                pk[k][i] = pack_cut(e0, e1);
-                e0 -= cut(e0);
-                e1 -= cut(e1);
-              }
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t* x2 = &sr[c >> 1][16 * (c & 1) + 2 * i];
+              const float2 x = ffma2(make_float2(__uint_as_float(x2[0]), __uint_as_float(x2[1])), sv, nv);
+              float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              ls = fadd2(ls, e);
+              pk[0][i] = pack_cut(e.x, e.y);
+              e = fadd2(e, make_float2(-cut(e.x), -cut(e.y)));
+              pk[1][i] = pack_cut(e.x, e.y);
+              e = fadd2(e, make_float2(-cut(e.x), -cut(e.y)));
+              pk[2][i] = pack_cut(e.x, e.y);
             }
 #pragma unroll
-            for (int k = 0; k < 3; ++k) tmem_st16_async(tS + 32 * k + 16 * c, pk[k]);
+            for (int k = 0; k < 3; ++k) tmem_st8_async(tS + 32 * k + 8 * c, pk[k]);
           }
-          l += ls[0] + ls[1];
+          l += ls.x + ls.y;
           tmem_wait_st();
           tc_fence_before();
         }
@@ -304,57 +313,66 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
     }
     if (!ok && lane == 0) pl.head->stale = 1;
   } else if (warp < kWarpMma) {
-    // ---- K (warps 4-7) or V (8-11), and half of Q each
+    // ---- K (warps 4-7) or V (8-11), and half of Q each.  A tile's loads are
+    // issued as soon as the last tile is stored, and cut in three as they
+    // arrive; what waits for the tensor core is the store alone.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegLoad));
     const bool is_v = warp >= 8;
     const int tid = threadIdx.x & 127;
-    const char* pool = (is_v ? p.v : p.k) + a.layer * p.layer_bytes();
-    // word c of row `row` of a part whose 64-element halves are `half_bytes` apart
-    auto place = [&](uint32_t base, int half_bytes, int row, int c) {
-      return base + (c >> 3) * half_bytes + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-    };
-    auto store3 = [&](uint32_t at, int part_bytes, const float4& x, const float4& y) {
-      uint4 w[3];
-      split8(x, y, w);
+    constexpr int RPW = 32 / CPR, STEP = 128 / CPR;  // rows of a warp, of the four warps, at a time
+    constexpr int WORDS = kKeys / STEP;              // 8-element words of a tile per thread
+    const int row0 = tid / CPR, c = tid % CPR;       // rows row0 + i STEP, word c
+    // the thread's word of row0: 64-element half, and place in it; the swizzle is
+    // the same in its other rows, which are multiples of 8 rows away
+    const uint32_t spot = c >> 3, swz = row0 * 128 + (((c & 7) ^ (row0 & 7)) << 4);
+    auto store3 = [&](uint32_t at, int part_bytes, const uint4 (&w)[3]) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(smem + at + k * part_bytes) = w[k];
     };
-    constexpr int WORDS = kKeys * CPR / 128;  // 8-element words of a tile per thread
-    float4 buf[2 * WORDS];
-    auto fetch = [&](int t) {
+    ItemWalk walk(pl, cta);
+    const char* pool = (is_v ? p.v : p.k) + a.layer * p.layer_bytes() + c * 32;
+    // page of the key that lane l looks up: row l % RPW of the warp's l / RPW-th rows
+    const int my_key = (tid >> 5) * RPW + lane % RPW + lane / RPW * STEP;
+    auto fetch_id = [&](int t) {
+      const int key = t * kKeys + my_key;
+      if (lane >= RPW * WORDS || key >= it.n_keys) return -1;
+      const int id = p.table[(int64_t)it.seq * p.max_pages + (key >> p.page_shift)];
+      if ((unsigned)id < (unsigned)p.n_pages) return id;
+      raise_on_plan(p, pl, ERR_BAD_INDEX, 133);
+      return -1;
+    };
+    uint4 parts[WORDS][3];
+    auto fetch = [&](int t, int ids) {
 #pragma unroll
-      for (int i = 0; i < WORDS; ++i) {
-        const int e = tid + 128 * i, row = e / CPR, c = e % CPR, key = t * kKeys + row;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (key < it.n_keys) {
-          const int id = p.table[(int64_t)it.seq * p.max_pages + (key >> p.page_shift)];
-          if ((unsigned)id < (unsigned)p.n_pages) {
-            const float4* src = reinterpret_cast<const float4*>(pool + id * p.page_bytes() + it.kv_head * p.head_bytes() +
-                                                               (int64_t)(key & (p.page_tokens - 1)) * (HD * 4)) + 2 * c;
-            x = __ldcg(src);
-            y = __ldcg(src + 1);
-          } else {
-            raise_on_plan(p, pl, ERR_BAD_INDEX, 133);
-          }
+      for (int i0 = 0; i0 < WORDS; i0 += WORDS / 2) {  // in two halves, for the registers
+        float4 buf[WORDS];
+#pragma unroll
+        for (int i = 0; i < WORDS / 2; ++i) {
+          const int key = t * kKeys + row0 + (i0 + i) * STEP, id = __shfl_sync(0xffffffffu, ids, (i0 + i) * RPW + lane / CPR);
+          const float4* src = reinterpret_cast<const float4*>(pool + id * p.page_bytes() + it.kv_head * p.head_bytes() +
+                                                              (int64_t)(key & (p.page_tokens - 1)) * (HD * 4));
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+          buf[2 * i] = id >= 0 ? __ldcg(src) : z;
+          buf[2 * i + 1] = id >= 0 ? __ldcg(src + 1) : z;
         }
-        buf[2 * i] = x;
-        buf[2 * i + 1] = y;
+#pragma unroll
+        for (int i = 0; i < WORDS / 2; ++i) split8(buf[2 * i], buf[2 * i + 1], parts[i0 + i]);
       }
     };
-    ItemWalk walk(pl, cta);
-    bool have = walk.next(&it), first = true, ok = true;
-    int t = walk.t0;
-    if (have) fetch(t);
+    bool have = walk.next(&it), ok = true;
+    int t = walk.t0, ids = have ? fetch_id(t) : -1;
+    bool first = true;
     for (uint32_t n = 0; have && ok; ++n) {
       if (first) {
         // Q: the S that read the last item's has to be over
         if (n > 0 && !(ok = mbar_wait_warp(bar(B_SFULL0 + ((n - 1) & 1u)), (n - 1) >> 1 & 1u, p.st, 134))) break;
-        constexpr int QW = kSlots / 2 * CPR / 128;  // words per thread
+        constexpr int QB = 4;  // words at a time
 #pragma unroll 1
-        for (int i0 = 0; i0 < QW; i0 += QW / 4) {
-          float4 q[QW / 2];
+        for (int i0 = 0; i0 < kSlots / 2 / STEP; i0 += QB) {
+          float4 q[2 * QB];
 #pragma unroll
-          for (int i = 0; i < QW / 4; ++i) {
-            const int e = tid + 128 * (i0 + i), row = (is_v ? kSlots / 2 : 0) + e / CPR, c = e % CPR, j = row / G;
+          for (int i = 0; i < QB; ++i) {
+            const int row = (is_v ? kSlots / 2 : 0) + row0 + (i0 + i) * STEP, j = row / G;
             q[2 * i] = q[2 * i + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j < it.n_rows && row < kSlots / G * G) {
               const float4* src = reinterpret_cast<const float4*>(
@@ -365,9 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
             }
           }
 #pragma unroll
-          for (int i = 0; i < QW / 4; ++i) {
-            const int e = tid + 128 * (i0 + i), row = (is_v ? kSlots / 2 : 0) + e / CPR, c = e % CPR;
-            store3(place(L::Q, L::QHALF, row, c), L::QPART, q[2 * i], q[2 * i + 1]);
+          for (int i = 0; i < QB; ++i) {
+            uint4 w[3];
+            split8(q[2 * i], q[2 * i + 1], w);
+            store3(L::Q + spot * L::QHALF + swz + ((is_v ? kSlots / 2 : 0) + (i0 + i) * STEP) * 128, L::QPART, w);
           }
         }
         fence_async_shared();
@@ -375,6 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
         if (lane == 0) mbar_arrive(bar(B_QFULL));
         first = false;
       }
+      fetch(t, ids);
+      // the next tile's pages
+      if (++t >= walk.t1) {
+        have = walk.next(&it);
+        t = walk.t0;
+        first = true;
+      }
+      ids = have ? fetch_id(t) : -1;
       // the product that read the last tile has to be over
       if (n > 0) {
         ok = is_v ? mbar_wait_warp(bar(B_PV), (n - 1) & 1u, p.st, 135)
@@ -382,21 +409,16 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
         if (!ok) break;
       }
 #pragma unroll
-      for (int i = 0; i < WORDS; ++i) {
-        const int e = tid + 128 * i, row = e / CPR, c = e % CPR;
-        store3(place(is_v ? L::V : L::K, L::KHALF, row, c), L::KPART, buf[2 * i], buf[2 * i + 1]);
-      }
+      for (int i = 0; i < WORDS; ++i)
+        store3((is_v ? L::V : L::K) + spot * L::KHALF + swz + i * STEP * 128, L::KPART, parts[i]);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(is_v ? B_VFULL : B_KFULL));
-      if (++t >= walk.t1) {
-        have = walk.next(&it);
-        t = walk.t0;
-        first = true;
-      }
-      if (have) fetch(t);
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegMma));
+  }
+  if (usable && warp == kWarpMma) {
     // ---- MMA issuer
     const bool leader = elect_one();
     constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;  // 8-row groups, version, 128-byte swizzle
@@ -406,7 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
     uint32_t n = 0, n_it = 0;
     bool ok = true;
     // the kept products, the small ones first
-    constexpr int kI[6] = {0, 1, 2, 0, 1, 0}, kJ[6] = {2, 1, 0, 1, 0, 0};
+    // (loops, not straight code: 72 products in a row are fetched slower than run)
+    constexpr uint32_t kI = 0x010210, kJ = 0x001012;  // of product x: part kI >> 4 x & 3 by kJ >> 4 x & 3
     auto issue_pv = [&](uint32_t m) -> bool {  // of tile m
       const uint32_t b = m & 1u;
       if (!mbar_wait_warp(bar(B_PFULL0 + b), m >> 1 & 1u, p.st, 137)) return false;
@@ -414,12 +437,13 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
       if (m > 0 && !mbar_wait_warp(bar(B_TFREE), (m - 1) & 1u, p.st, 142)) return false;
       tc_fence_after();
       if (leader) {
-#pragma unroll
-        for (int x = 0; x < 6; ++x)
+#pragma unroll 1
+        for (int x = 0; x < 6; ++x) {
+          const uint32_t pa = tmem + kColBuf * b + 32 * (kI >> 4 * x & 3), vb = v_lo + (kJ >> 4 * x & 3) * (L::KPART >> 4);
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            tc_mma_f16_ts(tmem + kColT, tmem + kColBuf * b + 32 * kI[x] + 8 * k,
-                          desc(v_lo + kJ[x] * (L::KPART >> 4) + k * 128), kIdescPV, x == 0 && k == 0 ? 0u : 1u);
+            tc_mma_f16_ts(tmem + kColT, pa + 8 * k, desc(vb + k * 128), kIdescPV, k == 0 ? (uint32_t)x : 1u);
+        }
         tc_commit(bar(B_PV));
       }
       __syncwarp();
@@ -431,13 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
         if (!(ok = mbar_wait_warp(bar(B_KFULL), n & 1u, p.st, 140))) break;
         tc_fence_after();
         if (leader) {
-#pragma unroll
-          for (int x = 0; x < 6; ++x)
+#pragma unroll 1
+          for (int x = 0; x < 6; ++x) {
+            const uint32_t qa = q_lo + (kI >> 4 * x & 3) * (L::QPART >> 4), kb = k_lo + (kJ >> 4 * x & 3) * (L::KPART >> 4);
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k)
-              tc_mma_f16(tmem + kColBuf * (n & 1u), desc(q_lo + (kI[x] * L::QPART + (k >> 2) * L::QHALF + (k & 3) * 32) / 16),
-                         desc(k_lo + (kJ[x] * L::KPART + (k >> 2) * L::KHALF + (k & 3) * 32) / 16), kIdescS,
-                         x == 0 && k == 0 ? 0u : 1u);
+              tc_mma_f16(tmem + kColBuf * (n & 1u), desc(qa + ((k >> 2) * L::QHALF + (k & 3) * 32) / 16),
+                         desc(kb + ((k >> 2) * L::KHALF + (k & 3) * 32) / 16), kIdescS, k == 0 ? (uint32_t)x : 1u);
+          }
           tc_commit(bar(B_SFULL0 + (n & 1u)));
         }
         __syncwarp();
