@@ -77,6 +77,16 @@ __device__ __forceinline__ void named_sync(int id) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(2 * kWG) : "memory");
 }
 
+// 32 bytes of a row: one full sector where rows are aligned to it
+__device__ __forceinline__ void store32(char* dst, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    st_global_v8(dst, w);
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return BF16 ? pack_bf162(lo, hi) : pack_half2(lo, hi);
@@ -137,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + lane_off + 128 * X, tO = tmem + lane_off + 256 + 128 * X;
     const float scale_log2 = a.scale * 1.4426950408889634f;
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)(a.o_stride * 2)) & 31) == 0;
     uint32_t n_xt = 0, n_xi = 0;
     bool ok = true;
     for (ItemWalk walk(pl, cta); walk.next(&it);) {
@@ -279,9 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 w[i] = pack2<BF16>(__uint_as_float(ov[16 * k + 2 * i]) * inv, __uint_as_float(ov[16 * k + 2 * i + 1]) * inv);
-              uint4* d4 = reinterpret_cast<uint4*>(dst + 64 * c + 32 * k);
-              d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              store32(dst + 64 * c + 32 * k, w, wide);
             }
           } else if (valid) {
 #pragma unroll
@@ -336,9 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[2 * i] = pack2<BF16>(acc[i].x * inv, acc[i].y * inv);
           w[2 * i + 1] = pack2<BF16>(acc[i].z * inv, acc[i].w * inv);
         }
-        uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * k);
-        d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        store32(dst + 32 * k, w, wide);
       }
       if (states && a.lse)
         a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
