@@ -414,7 +414,7 @@ typedef struct {
                           * table[seq][t / page_tokens]; entries behind its length are not read */
   int32_t *length;       /* [n_seqs] tokens; an unused sequence has 0 */
   int32_t *refs;         /* [n_pages] sequences that hold the page; 0: free */
-  void *status;          /* 16 bytes, 16-byte aligned, zeroed once by the caller */
+  void *status;          /* 16 bytes, 16-byte aligned, zeroed once by the caller, then the library's */
   void *workspace;       /* duolm_pages_workspace() bytes, 16-byte aligned, any contents */
   int64_t workspace_bytes;
 } duolm_pages;
@@ -503,13 +503,17 @@ int duolm_pages_plan(const duolm_pages *pages, const duolm_pages_batch *batch, v
 /*
  * duolm_pages_write: a layer's projections into the cache.  Every q and k head
  * is RMS-normalised over head_dim (gains q_gain, k_gain: device float
- * [head_dim], 16-byte aligned, NULL: no norm) and its pairs (i, i + head_dim / 2) are rotated
- * by rope[position][i] = (cos, sin) (device float [rope_positions][head_dim /
- * 2][2], 16-byte aligned, NULL: no rotation), in fp32, rounded once.  k goes
- * to its token's slot, v there unchanged, q to q_out (which may be q).
+ * [head_dim], 16-byte aligned, NULL: no norm) and its pairs (i, i + head_dim /
+ * 2) are rotated by rope[position][i] = (cos, sin) (device float
+ * [rope_positions][head_dim / 2][2], 16-byte aligned, NULL: no rotation), in
+ * fp32, rounded once.  k goes to its token's slot, v there unchanged, q to
+ * q_out (which may be q).
  *   q, q_out: [n_rows][n_q_heads][head_dim], NULL q: K and V only;
  *   k, v: [n_rows][n_kv_heads][head_dim]; elements of the cache's dtype.
  * Strides are elements from row to row; rows must be 16-byte aligned.
+ * A page that several sequences hold is written for all of them:
+ * duolm_pages_resize copies it when a sequence grows out of it, so rows that
+ * were added by the last resize are the sequence's own.
  * Raises: an entry with more rows than its sequence has tokens, a position
  * not in rope.
  */

@@ -11,7 +11,7 @@
 
 #include <cstdarg>
 #include <cstdio>
-#include <mutex>
+#include <atomic>
 #include <string>
 
 // reason of the calling thread's last failed context-free call (runtime.cu)
@@ -25,18 +25,20 @@ int pages_fail(int code, const char* fmt, ...) {
   va_start(ap, fmt);
   std::vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  g_noctx_err = buf;
+  try {
+    g_noctx_err = buf;
+  } catch (...) {  // no memory for the reason: the code has to do
+  }
   return code;
 }
 
 int pages_sms(int device) {
-  static std::mutex mu;
-  static int sms[64] = {};
-  if (device < 0 || device >= 64) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!sms[device] && cudaDeviceGetAttribute(&sms[device], cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
-    sms[device] = 0;
-  return sms[device];
+  static std::atomic<int> sms[kMaxDevices];
+  if (device < 0 || device >= kMaxDevices) return 0;
+  int n = sms[device].load(std::memory_order_relaxed);
+  if (!n && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) == cudaSuccess)
+    sms[device].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 int pages_view(const duolm_pages* p, PagesView* out) {
@@ -459,31 +461,44 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(PagesView p, int n, cons
 // in any order, and the old copies stay as they were.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void compact_decide(const PagesView& p, const PagesWork& w, int32_t* live_out, int* s_scan) {
+  constexpr int kIds = 4;  // pages of a thread at a time
   int mine = 0, live;
   for (int64_t id = threadIdx.x; id < p.n_pages; id += kThreads) mine += p.refs[id] > 0;
   block_scan<kThreads>(mine, s_scan, &live);
   int holes = 0, moved = 0;
-  for (int64_t b = 0; b < p.n_pages; b += kThreads) {
-    const int64_t id = b + threadIdx.x;
-    const int r = id < p.n_pages ? p.refs[id] : 0;
-    const bool hole = id < live && r <= 0, mover = id >= live && id < p.n_pages && r > 0;
-    int all;
+  for (int64_t b = 0; b < p.n_pages; b += kIds * kThreads) {
+    const int64_t id0 = b + kIds * threadIdx.x;
+    int r[kIds], n_holes = 0, n_movers = 0;
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+      const int64_t id = id0 + j;
+      r[j] = id < p.n_pages ? p.refs[id] : 0;
+      n_holes += id < live && r[j] <= 0;
+      n_movers += id >= live && r[j] > 0;
+    }
+    int all, at = 0, to = 0;
     if (b < live) {
-      const int at = block_scan<kThreads>(hole, s_scan, &all);
-      if (hole) w.copies[holes + at].dst = (int)id;
+      at = holes + block_scan<kThreads>(n_holes, s_scan, &all);
       holes += all;
     }
-    if (b + kThreads > live) {
-      const int at = block_scan<kThreads>(mover, s_scan, &all);
-      if (mover) {
-        PageCopy& c = w.copies[moved + at];
-        c.src = (int)id;
-        c.rows = p.page_tokens;
-        c.refs = r;
-      }
+    if (b + kIds * kThreads > live) {
+      to = moved + block_scan<kThreads>(n_movers, s_scan, &all);
       moved += all;
     }
-    if (id < p.n_pages && !mover) w.map[id] = id < live && r > 0 ? (int)id : -1;
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+      const int64_t id = id0 + j;
+      if (id >= p.n_pages) break;
+      if (id >= live && r[j] > 0) {
+        PageCopy& c = w.copies[to++];
+        c.src = (int)id;
+        c.rows = p.page_tokens;
+        c.refs = r[j];
+      } else {
+        w.map[id] = id < live && r[j] > 0 ? (int)id : -1;
+        if (id < live && r[j] <= 0) w.copies[at++].dst = (int)id;
+      }
+    }
   }
   __syncthreads();
   for (int k = threadIdx.x; k < moved; k += kThreads) w.map[w.copies[k].src] = w.copies[k].dst;
@@ -542,17 +557,10 @@ size_t seen_bytes(const PagesView& p) { return (size_t)((p.n_seqs + 31) / 32) * 
 // bitmap of the largest cache (2^20 sequences: 128 KB), whichever is larger.
 constexpr int kMaxSmem = kRingBytes > 128 * 1024 ? kRingBytes : 128 * 1024;
 cudaError_t allow_smem(int device) {
-  static std::mutex mu;
-  static bool raised[64] = {};
-  std::lock_guard<std::mutex> lock(mu);
-  if (raised[device]) return cudaSuccess;
-  for (const void* f : {reinterpret_cast<const void*>(resize_kernel), reinterpret_cast<const void*>(fork_kernel),
-                        reinterpret_cast<const void*>(compact_kernel)}) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e != cudaSuccess) return e;
-  }
-  raised[device] = true;
-  return cudaSuccess;
+  static SmemRaised resize, fork, compact;
+  cudaError_t e = resize.raise(resize_kernel, kMaxSmem, device);
+  if (e == cudaSuccess) e = fork.raise(fork_kernel, kMaxSmem, device);
+  return e == cudaSuccess ? compact.raise(compact_kernel, kMaxSmem, device) : e;
 }
 
 int launched(cudaError_t e, const char* what) {

@@ -13,6 +13,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "duolm.h"
@@ -291,6 +292,7 @@ struct AttnArgs {
   int64_t q_stride, o_stride;  // elements between rows
   int n_q_heads, group, causal, layer;
   float scale;
+  int device;
 };
 cudaError_t pages_attention_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool few, cudaStream_t s);
 // fp32 of head_dim 64 and 128 (pages_attention_f32.cu)
@@ -299,6 +301,19 @@ cudaError_t pages_attention_f32(const PagesView& p, const PagesPlan& pl, const A
 cudaError_t pages_attention_few(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, cudaStream_t s);
 cudaError_t pages_attention_tc(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, bool bf16, int n_rows,
                                cudaStream_t s);
+
+// A kernel's dynamic shared memory, raised once per device.
+constexpr int kMaxDevices = 64;
+struct SmemRaised {
+  std::atomic<bool> done[kMaxDevices];
+  template <typename... KArgs>
+  cudaError_t raise(void (*kernel)(KArgs...), int bytes, int device) {
+    if (done[device].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[device].store(true, std::memory_order_release);
+    return e;
+  }
+};
 
 // host helpers (pages.cu)
 int pages_fail(int code, const char* fmt, ...);

@@ -256,7 +256,8 @@ namespace {
 template <int M, int NC>
 cudaError_t launch_simt(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
   const size_t smem = 4 * (size_t)(M * (p.head_dim + 4) + kTile * (p.head_dim + 4) + kTile * p.head_dim + M * (kTile + 4));
-  cudaError_t e = cudaFuncSetAttribute(attention_simt_kernel<M, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+  static SmemRaised raised;
+  const cudaError_t e = raised.raise(attention_simt_kernel<M, NC>, 224 * 1024, a.device);
   if (e != cudaSuccess) return e;
   return launch_ex(attention_simt_kernel<M, NC>, dim3(pl.ctas), dim3(kThreads), smem, s, true, p, pl, a);
 }

@@ -485,8 +485,8 @@ namespace {
 
 template <int HD>
 cudaError_t launch_f32(const PagesView& p, const PagesPlan& pl, const AttnArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(pages_attention_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Lay<HD>::SMEM);
+  static SmemRaised raised;
+  const cudaError_t e = raised.raise(pages_attention_f32_kernel<HD>, Lay<HD>::SMEM, a.device);
   if (e != cudaSuccess) return e;
   return launch_ex(pages_attention_f32_kernel<HD>, dim3(pl.ctas), dim3(kThreads), Lay<HD>::SMEM, s, true, p, pl, a);
 }

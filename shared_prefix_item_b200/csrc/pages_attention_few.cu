@@ -348,8 +348,8 @@ namespace {
 template <int HD, bool BF16>
 cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const PagesView& p, const PagesPlan& pl,
                        const AttnArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(pages_attention_few_kernel<HD, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Lay<HD>::SMEM);
+  static SmemRaised raised;
+  const cudaError_t e = raised.raise(pages_attention_few_kernel<HD, BF16>, Lay<HD>::SMEM, a.device);
   if (e != cudaSuccess) return e;
   return launch_ex(pages_attention_few_kernel<HD, BF16>, dim3(pl.ctas), dim3(kThreads), Lay<HD>::SMEM, s, true, tk, tv, p,
                    pl, a);

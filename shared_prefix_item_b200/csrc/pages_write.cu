@@ -502,9 +502,8 @@ extern "C" int duolm_pages_plan(const duolm_pages* pages, const duolm_pages_batc
   const size_t smem = (size_t)((p.n_seqs + 31) / 32) * 4;
   // a CTA per kPlanThreads rows, and per half as many items, which take longer
   const int grid = std::min(std::max((batch->n_rows + kPlanThreads - 1) / kPlanThreads, (2 * pl.max_items + kPlanThreads - 1) / kPlanThreads), sms);
-  cudaError_t e = cudaSuccess;
-  if (smem > 14 * 1024)  // with 33 KB of its own
-    e = cudaFuncSetAttribute(batch_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  static SmemRaised raised;  // (33 KB are static)
+  cudaError_t e = raised.raise(batch_plan_kernel, 128 * 1024, pages->device);
   if (e == cudaSuccess)
     e = launch_ex(batch_plan_kernel, dim3(grid), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(cuda_stream), true,
                   p, b, pl, sh.tokens(group), sh.keys, sh.grain, sh.few);
@@ -582,7 +581,7 @@ extern "C" int duolm_pages_attention(const duolm_pages* pages, const duolm_pages
   DeviceGuard g(pages->device);
   if (!g.ok()) return pages_fail(DUOLM_E_CUDA, "pages_attention: device %d", pages->device);
   const AttnArgs a{static_cast<const char*>(q), static_cast<char*>(out), lse, q_stride, out_stride, batch->n_q_heads,
-                   batch->n_q_heads / p.n_kv_heads, batch->causal != 0, layer, scale};
+                   batch->n_q_heads / p.n_kv_heads, batch->causal != 0, layer, scale, pages->device};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool bf16 = pages->dtype == DUOLM_DTYPE_BF16;
   cudaError_t e;

@@ -234,6 +234,39 @@ def test_many_sequences_and_pages_cross_the_planner_s_blocks():
     c.same()
 
 
+def test_copies_and_moves_of_a_whole_grid():
+    """Enough page copies, and then moves, for every SM: what each sequence
+    holds is what it held, in every layer."""
+    torch = _t()
+    c = Cache("bf16", layers=8, heads=4, hd=64, page=16, n_pages=700, n_seqs=80, max_pages=8)
+    src = list(range(16))
+    c.resize(src, [17 + 5 * i for i in src])
+    c.fill(gen(21))
+    held = {s: [[x.clone() for x in c.kv(l, s)] for l in range(8)] for s in src}
+    dst = list(range(16, 80))
+    take = [c.book.length[d % 16] - (d % 3) for d in dst]
+    c.fork([d % 16 for d in dst], dst, take)
+    copies = c.resize(dst, [t + 3 for t in take])
+    assert len(copies) > 50
+    c.same()
+
+    def check():
+        for s in src + dst:
+            n = c.book.length[s] if s in src else take[dst.index(s)]
+            for l in range(8):
+                for got, want in zip(c.kv(l, s), held[s if s in src else s % 16][l]):
+                    assert torch.equal(got[:, :n], want[:, :n]), (s, l)
+    check()
+    c.free(src[::2] + dst[::3])
+    src, gone = src[1::2], set(dst[::3])
+    take, dst = [t for t, d in zip(take, dst) if d not in gone], [d for d in dst if d not in gone]
+    live = ints([0])
+    c.c.compact(c.table, c.refs, live)
+    assert c.book.compact()
+    c.same()
+    check()
+
+
 # ---- refusals on the device ----------------------------------------------------
 
 def _refused(c, code, call):
@@ -295,6 +328,34 @@ def test_a_refused_plan_runs_nothing(seqs, off):
     assert bool((out == 5.0).all())
     b.plan()
     b.attention(0, q, out, None, 0.125)
+    c.c.check()
+    assert not bool((out == 5.0).any())
+
+
+def test_a_plan_of_other_sizes_is_refused():
+    import shared_prefix_item_b200 as S
+    torch = _t()
+    c = Cache(n_pages=16, n_seqs=8, max_pages=16)
+    c.resize([0, 3], [20, 1])
+    c.fill(gen(3))
+    q = torch.randn((3, 4, 64), device="cuda").half()
+    plan = torch.full((64 << 20,), 0x33, dtype=torch.uint8, device="cuda")
+    one = c.c.batch(ints([0, 3]), ints([0, 2, 3]), 3, 2, 4, plan)
+    others = [c.c.batch(ints([0, 3]), ints([0, 2, 3]), 3, 2, 4, plan, causal=False),
+              c.c.batch(ints([0]), ints([0, 2]), 3, 2, 4, plan), c.c.batch(ints([0, 3]), ints([0, 2, 3]), 3, 9, 4, plan)]
+
+    def refused(b):
+        out = torch.full_like(q, 5.0)
+        b.attention(0, q, out, None, 0.125)
+        with pytest.raises(S.DuolmError) as e:
+            c.c.check()
+        assert e.value.code == -8 and bool((out == 5.0).all())
+    refused(one)  # the buffer holds no plan at all
+    one.plan()
+    for b in others:
+        refused(b)
+    out = torch.full_like(q, 5.0)
+    one.attention(0, q, out, None, 0.125)
     c.c.check()
     assert not bool((out == 5.0).any())
 
@@ -483,7 +544,7 @@ def test_attention_of_a_few_tokens_each(dt):
 
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("hd, heads, group, page", [(128, 2, 2, 16), (64, 2, 1, 8), (64, 1, 7, 64), (128, 1, 4, 256),
-                                                    (128, 1, 64, 32), (64, 2, 3, 128)])
+                                                    (128, 1, 64, 32), (64, 2, 3, 128), (128, 2, 5, 8)])
 def test_attention_of_chunks(dt, hd, heads, group, page):
     _check_attention(dt, hd, heads, group, page, [1, 5, 64, 65, 130, 0, 200, 33], [1, 5, 100, 65, 513, 7, 200, 1000])
 
@@ -528,6 +589,45 @@ def test_attention_of_a_larger_entry_than_said(dt):
 def test_attention_of_flat_rows_and_another_layer(dt):
     _check_attention(dt, 64, 2, 2, 16, [1, 40], [70, 90], flat=True, layers=3)
     _check_attention(dt, 128, 2, 2, 16, [1, 2], [70, 90], flat=True, layers=2)
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_attention_of_rows_aligned_to_16_bytes_alone(dt):
+    torch = _t()
+    g = gen(31)
+    c = Cache(dt, heads=1, hd=64, n_pages=40, n_seqs=2, max_pages=20)
+    c.resize([1, 0], [300, 70])
+    c.fill(g)
+    e = 16 // c.k.element_size()
+    for rows in ([150, 70], [2, 1]):
+        b, off, n = c.batch([1, 0], rows, 2)
+        b.plan()
+        wide = torch.randn((n, 128 + e), generator=g, device="cuda").to(c.dt)
+        buf = torch.full((n, 128 + e), 9.0, device="cuda", dtype=c.dt)
+        q, out = wide[:, e:], buf[:, e:]
+        b.attention(0, q, out, None, 0.125)
+        c.c.check()
+        assert bool((buf[:, :e] == 9.0).all())
+        for i, s in enumerate([1, 0]):
+            want, _, bound, _ = paged.attention(c.dt, q[off[i]:off[i + 1]].reshape(-1, 2, 64), *c.kv(0, s), 0.125, rows[i],
+                                                c.book.length[s], True)
+            assert bool(((out[off[i]:off[i + 1]].reshape(-1, 2, 64).double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("rows", [1, 64])
+def test_attention_of_more_tiles_than_are_taken_by_the_unit(dt, rows):
+    """Long enough for the CTAs' shares to be cut tile by tile."""
+    _check_attention(dt, 64, 4, 2, 64, [rows] * 16, [9000 + 37 * i for i in range(16)])
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("rows", [1, 9])
+def test_attention_of_more_entries_than_one_cta_plans(dt, rows):
+    r = random.Random(7)
+    n = 1500
+    _check_attention(dt, 64, 1, 2, 8, [r.choice([0, 1, rows, rows]) for _ in range(n)], [r.randint(0, 60) for _ in range(n)],
+                     max_rows=rows)
 
 
 @pytest.mark.parametrize("hd", [32, 96, 160, 192, 224, 256])
@@ -665,6 +765,54 @@ def test_a_captured_step_goes_on_as_the_lengths_do(dt, rows):
             assert torch.equal(K[:, lens[i] - rows:].transpose(0, 1), k[lo:hi])
             want, _, bound, _ = paged.attention(c.dt, q[lo:hi], K, V, hd ** -0.5, rows, lens[i], True)
             assert bool(((out[lo:hi].double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("layers", [1, 6])
+def test_a_captured_fork_and_compaction(layers):
+    """free, fork, resize and compact captured once, replayed over other lengths
+    (one layer: a cluster of CTAs; six: a whole grid)."""
+    torch = _t()
+    n = 24
+    c = Cache("fp16", layers=layers, heads=4, hd=64, page=8, n_pages=600, n_seqs=2 * n, max_pages=12)
+    src, dst = list(range(n)), list(range(n, 2 * n))
+    s_src, s_dst, take, grown, live = ints(src), ints(dst), ints([0] * n), ints([1] * n), ints([0])
+    c.resize(src, [5] * n)
+    side = torch.cuda.Stream()
+
+    def step(stream):
+        c.c.free(s_dst, stream)
+        c.c.fork(s_src, s_dst, take, stream)
+        c.c.resize(s_dst, grown, stream)
+        c.c.compact(c.table, c.refs, live, stream)
+
+    def book(t, g):
+        c.book.resize(dst, [0] * n)
+        c.book.fork(src, dst, t)
+        c.book.resize(dst, g)
+        c.book.compact()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step(side.cuda_stream)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(side.cuda_stream)
+    book([0] * n, [1] * n)
+    r = random.Random(layers)
+    for _ in range(4):
+        c.resize(src, [r.randint(1, 60) for _ in src])
+        c.fill(gen(41))
+        held = [[x.clone() for x in c.kv(layers - 1, s)] for s in src]
+        t = [r.randint(0, c.book.length[s]) for s in src]
+        g = [x + r.randint(0, 20) for x in t]
+        take.copy_(ints(t))
+        grown.copy_(ints(g))
+        graph.replay()
+        book(t, g)
+        c.same()
+        for i in range(n):
+            for got, src_kv, want in zip(c.kv(layers - 1, dst[i]), c.kv(layers - 1, src[i]), held[i]):
+                assert torch.equal(got[:, : t[i]], want[:, : t[i]]) and torch.equal(src_kv, want)
 
 
 def test_calls_follow_their_stream():

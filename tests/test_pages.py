@@ -102,7 +102,7 @@ def test_a_bad_batch_is_refused(over, code):
     dict(layer=-1), dict(layer=2), dict(k=None), dict(v=None), dict(q_out=None), dict(q_stride=255), dict(k_stride=127),
     dict(v_stride=120), dict(q_out_stride=248), dict(q=A + 8), dict(k=A + 2), dict(v=A + 4), dict(q_out=A + 8),
     dict(q_stride=260), dict(k_stride=132), dict(rope=A + 8, rope_positions=4), dict(rope=A, rope_positions=0),
-    dict(eps=-1.0), dict(eps=float("nan"))])
+    dict(eps=-1.0), dict(eps=float("nan")), dict(q_gain=A + 4), dict(k_gain=A + 8)])
 def test_bad_write_arguments_are_refused(over):
     f = dict(layer=0, q=A, q_stride=256, k=A, k_stride=128, v=A, v_stride=128, q_gain=None, k_gain=None, eps=1e-6,
              rope=None, rope_positions=0, q_out=A, q_out_stride=256)
