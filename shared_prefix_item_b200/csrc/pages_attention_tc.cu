@@ -31,10 +31,6 @@
 //             runs, eight products cost 512.  The warp also zeroes V rows behind
 //             the last visible key: P is 0 there, but the slots may hold
 //             anything, and 0 x NaN is NaN.
-// A step is what the issuer does for one K/V tile; one commit at its end frees
-// K of this step's tile and V of the tiles whose P V it ran.  A barrier's phase
-// can be waited for only while it is the current or the last one, so one warp
-// (8) sees every step in turn and tells warp 11 which V slots are free.
 // Tensor memory: S/P of A in columns [0, 128), of B in [128, 256), O of A from
 // 256, of B from 384.  tcgen05.mma of one thread run in issue order, so S_X may
 // be issued right behind the P V that reads the same columns, and its commit
@@ -68,8 +64,8 @@ struct Lay {
 };
 
 enum { B_QFULL0, B_QFULL1, B_QEMPTY0, B_QEMPTY1, B_SFULL0, B_SFULL1, B_PFULL0, B_PFULL1, B_OFULL0, B_OFULL1, B_DRAIN, B_KV };
-// then per slot: K full, V full, step done, V free
-enum { KFULL, VFULL, STEP, VFREE };
+// then per slot
+enum { KFULL, VFULL, KEMPTY, VEMPTY };
 template <int HD>
 __device__ __forceinline__ int kv_bar(int kind, uint32_t slot) { return B_KV + kind * Lay<HD>::SLOTS + slot; }
 
@@ -375,37 +371,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ((id * p.n_kv_heads + it.kv_head) << p.page_shift) + ((t * kKeys + bj * box) & (p.page_tokens - 1)));
     };
     if (warp == kWarpK) {
-      // n: K tiles loaded; seen: steps seen; nv: V slots handed on; lane i has
-      // the step that frees V of the last tile k with k % 32 == i
-      uint32_t n = 0, seen = 0, nv = 0, frees = 0;
+      uint32_t n = 0;
       bool ok = true;
-      auto free_v = [&]() {
-        while (nv < n && (nv < SLOTS || __shfl_sync(0xffffffffu, frees, (nv - SLOTS) & 31) < seen)) {
-          if (lane == 0) mbar_arrive(kvbar(VFREE, nv % SLOTS));
-          ++nv;
-        }
-      };
       for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
-        const bool two = it.n_rows > sub_tokens;
-        const uint32_t end = n + (walk.t1 - walk.t0);  // the next item's first step
         int id = fetch(walk.t0);
-        for (int t = walk.t0; t < walk.t1; ++t) {
+        for (int t = walk.t0; t < walk.t1; ++t, ++n) {
           const uint32_t slot = n % SLOTS;
           const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
-          if (n >= SLOTS) {
-            if (!(ok = mbar_wait_warp(kvbar(STEP, slot), (n / SLOTS - 1) & 1u, p.st, 104))) break;
-            ++seen;
-          }
+          if (!(ok = mbar_wait_warp(kvbar(KEMPTY, slot), (n / SLOTS & 1u) ^ 1u, p.st, 104))) break;
           load_tile(&tmK, t, id, sbase + L::K + slot * NH * kHalf, kvbar(KFULL, slot));
-          if (lane == (int)(n & 31)) frees = two ? n + 1 : min(n + 2, end);
-          ++n;
-          free_v();
           id = next_id;
         }
-      }
-      for (; ok && nv < n; free_v()) {
-        if (!(ok = mbar_wait_warp(kvbar(STEP, seen % SLOTS), seen / SLOTS & 1u, p.st, 104))) break;
-        ++seen;
       }
       if (!ok)  // leave no copy in flight into shared memory that this CTA gives up
         for (uint32_t k = n > SLOTS ? n - SLOTS : 0; k < n; ++k)
@@ -429,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = walk.t0; ok && t < walk.t1; ++t, ++n) {
           const uint32_t slot = n % SLOTS;
           const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
-          if (!(ok = mbar_wait_warp(kvbar(VFREE, slot), n / SLOTS & 1u, p.st, 105))) break;
+          if (!(ok = mbar_wait_warp(kvbar(VEMPTY, slot), (n / SLOTS & 1u) ^ 1u, p.st, 105))) break;
           load_tile(&tmV, t, id, sbase + L::V + slot * NH * kHalf, kvbar(VFULL, slot));
           id = next_id;
         }
@@ -474,7 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_lo = ((sbase + L::Q) >> 4) | 1u << 16, k_lo = ((sbase + L::K) >> 4) | 1u << 16,
                      v_lo = ((sbase + L::V) >> 4) | (uint32_t)(kHalf >> 4) << 16;
       // P V of a chain's last tile, issued before its next S: bit 0 there is
-      // one, 1 the item's first tile of the chain, 2 its last, 8.. the slot
+      // one, 1 the item's first tile of the chain, 2 its last, 3 V is free behind
+      // it, 8.. the slot
       uint32_t pend_a = 0, pend_b = 0, xt_a = 0, xt_b = 0;  // xt: P V issued
       uint32_t n = 0, nq = 0;
       bool ok = true;
@@ -488,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kKeys / 16; ++k)
             tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? ~pend & 2u : 1u);
           if (pend & 4u) tc_commit(bar(B_OFULL0 + X));
+          if (pend & 8u) tc_commit(kvbar(VEMPTY, pend >> 8));
         }
         __syncwarp();
         if (X) ++xt_b; else ++xt_a;
@@ -523,14 +501,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
               const int step = two ? 1 : 2;
-              pend = 1u | (lt < step ? 2u : 0u) | (lt + step >= nt ? 4u : 0u) | slot << 8;
+              pend = 1u | (lt < step ? 2u : 0u) | (lt + step >= nt ? 4u : 0u) | (!two || X ? 8u : 0u) | slot << 8;
             }
             if (X)
               pend_b = pend;
             else
               pend_a = pend;
           }
-          if (ok && leader) tc_commit(kvbar(STEP, slot));
+          if (ok && leader) tc_commit(kvbar(KEMPTY, slot));
         }
         nq += two ? 2 : 1;
         // the item's last P V, before anything waits for the next item's K
