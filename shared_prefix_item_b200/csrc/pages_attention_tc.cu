@@ -173,10 +173,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_vis = vis - (walk.t0 + lt) * kKeys;  // of this tile
         if (__any_sync(0xffffffffu, n_vis < kKeys)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            if (!__any_sync(0xffffffffu, n_vis < 32 * (c + 1))) continue;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * c + i >= n_vis) sr[c][i] = __float_as_uint(-INFINITY);
+          }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -511,9 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && leader) tc_commit(kvbar(KEMPTY, slot));
         }
         nq += two ? 2 : 1;
-        // the item's last P V, before anything waits for the next item's K
-        if (ok && pend_a) ok = issue_pv(0, pend_a);
-        if (ok && pend_b) ok = issue_pv(1, pend_b);
+        // the item's last P V, before anything waits for the next item's K, the
+        // chain of the last tile last
+        const bool b_first = !two && (nt & 1);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int X = b_first ? 1 - i : i;
+          const uint32_t pend = X ? pend_b : pend_a;
+          if (ok && pend) ok = issue_pv(X, pend);
+        }
         pend_a = pend_b = 0;
       }
       // no tensor-core operation of this CTA may outlive its TMEM
