@@ -51,7 +51,7 @@ constexpr int kRegLaunch = 168, kRegSoftmax = 200, kRegOther = 104;
 static_assert(2 * kWG * kRegSoftmax + kWG * kRegOther <= kThreads * kRegLaunch, "register split above the launch's registers");
 constexpr int kHalf = 16384;  // 128 rows x 64 elements
 constexpr uint32_t kTmemCols = 512;
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kSumLimit = 256.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int HD>
@@ -81,6 +81,15 @@ __device__ __forceinline__ void store32(char* dst, const uint32_t (&w)[8], bool 
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+
+// mbar_wait_warp with the usual case inline and the rest in one place: the
+// issuing warp's instructions are part of every step.
+__device__ __noinline__ bool slow_wait(uint32_t b, uint32_t parity, DevStatus* st, uint32_t where) {
+  return mbar_wait_warp(b, parity, st, where);
+}
+__device__ __forceinline__ bool fast_wait(uint32_t b, uint32_t parity, DevStatus* st, uint32_t where) {
+  return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) || slow_wait(b, parity, st, where);
 }
 
 template <bool BF16>
@@ -180,46 +189,59 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (32 * c + i >= n_vis) sr[c][i] = __float_as_uint(-INFINITY);
           }
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // The weights go by the running maximum of the tiles before, and where
+        // their sum stays within 2^8 that stands: none is above 2^8 (P fits its
+        // type) and none that matters is lost.  Otherwise, in the first tile,
+        // and where the row has seen no key yet, the tile's maximum is taken and
+        // O and l are rescaled: decided for the whole warp, as the rescale is
+        // warp-collective, by its own rows alone (slots of no row hold what
+        // shared memory held).  The exponentials' instructions bound a chain,
+        // so the 64 of a maximum per tile count.
+        const float2 sv = make_float2(scale_log2, scale_log2);
+        float2 ls[2];
+        for (bool max_first = lt == first;; max_first = true) {
+          if (max_first) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx[(i >> 1) & 3] = fmax3f(mx[(i >> 1) & 3], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
-        const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2);
-        // decided for the whole warp, as the rescale is warp-collective, by its
-        // own rows alone: slots of no row hold what shared memory held
-        if (lt == first) {
-          m_used = m_new;
-        } else if (__any_sync(0xffffffffu, valid && m_new > m_used + kRescaleLog2)) {
-          const float corr = m_new == m_used ? 1.f : fast_exp2(m_used - m_new);
+              for (int i = 0; i < 32; i += 2)
+                mx[(i >> 1) & 3] = fmax3f(mx[(i >> 1) & 3], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+            const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2);
+            if (lt != first) {
+              const float corr = m_new == m_used ? 1.f : fast_exp2(m_used - m_new);
 #pragma unroll 1
-          for (int c = 0; c < HD / 32; ++c) {
-            float v[32];
-            tmem_ld32(tO + 32 * c, v);
+              for (int c = 0; c < HD / 32; ++c) {
+                float v[32];
+                tmem_ld32(tO + 32 * c, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= corr;
-            tmem_st32(tO + 32 * c, v);
+                for (int i = 0; i < 32; ++i) v[i] *= corr;
+                tmem_st32(tO + 32 * c, v);
+              }
+              l *= corr;
+            }
+            m_used = m_new;
           }
-          l *= corr;
-          m_used = m_new;
-        }
-        const float nmu = m_used == -INFINITY ? 0.f : -m_used;  // no key of this row yet
-        const float2 sv = make_float2(scale_log2, scale_log2), nv = make_float2(nmu, nmu);
-        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float nmu = m_used == -INFINITY ? 0.f : -m_used;  // no key of this row yet
+          const float2 nv = make_float2(nmu, nmu);
+          ls[0] = ls[1] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = ffma2(make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])), sv, nv);
-            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            ls[i & 1] = fadd2(ls[i & 1], e);
-            pk[i] = pack2<BF16>(e.x, e.y);
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = ffma2(make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])), sv, nv);
+              const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              ls[i & 1] = fadd2(ls[i & 1], e);
+              pk[i] = pack2<BF16>(e.x, e.y);
+            }
+            tmem_st16_async(tS + 16 * c, pk);
           }
-          tmem_st16_async(tS + 16 * c, pk);
+          ls[0] = fadd2(ls[0], ls[1]);
+          if (max_first || !__any_sync(0xffffffffu, valid && (ls[0].x + ls[0].y > kSumLimit || (m_used == -INFINITY && n_vis > 0))))
+            break;
         }
-        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        l += ls[0].x + ls[0].y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -451,78 +473,120 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto desc = [](uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; };
       const uint32_t q_lo = ((sbase + L::Q) >> 4) | 1u << 16, k_lo = ((sbase + L::K) >> 4) | 1u << 16,
                      v_lo = ((sbase + L::V) >> 4) | (uint32_t)(kHalf >> 4) << 16;
-      // P V of a chain's last tile, issued before its next S: bit 0 there is
-      // one, 1 the item's first tile of the chain, 2 its last, 3 V is free behind
-      // it, 8.. the slot
-      uint32_t pend_a = 0, pend_b = 0, xt_a = 0, xt_b = 0;  // xt: P V issued
-      uint32_t n = 0, nq = 0;
+      uint32_t n = 0, nq = 0, xt_a = 0, xt_b = 0;  // xt: P V issued
       bool ok = true;
-      auto issue_pv = [&](int X, uint32_t pend) -> bool {
-        if (!mbar_wait_warp(bar(B_PFULL0 + X), (X ? xt_b : xt_a) & 1u, p.st, 108)) return false;
-        tc_fence_after();
-        const uint32_t tS = tmem + 128 * X, tO = tmem + 256 + 128 * X;
-        const uint32_t v = v_lo + (pend >> 8) * (NH * kHalf >> 4);
-        if (leader) {
+      auto pv = [&](int X, uint32_t slot, uint32_t accumulate) {
+        const uint32_t tS = tmem + 128 * X, tO = tmem + 256 + 128 * X, v = v_lo + slot * (NH * kHalf >> 4);
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? ~pend & 2u : 1u);
-          if (pend & 4u) tc_commit(bar(B_OFULL0 + X));
-          if (pend & 8u) tc_commit(kvbar(VEMPTY, pend >> 8));
+        for (int k = 0; k < kKeys / 16; ++k) tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? accumulate : 1u);
+      };
+      auto score = [&](int X, uint32_t qb, uint32_t slot) {
+        const uint32_t q = q_lo + qb * (NH * kHalf >> 4), k0 = k_lo + slot * (NH * kHalf >> 4);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t o = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+          tc_mma_f16(tmem + 128 * X, desc(q + o), desc(k0 + o), kIdescS, k > 0 ? 1u : 0u);
         }
-        __syncwarp();
+        tc_commit(bar(B_SFULL0 + X));
+      };
+      auto wait_p = [&](int X) {
+        ok = ok && fast_wait(bar(B_PFULL0 + X), (X ? xt_b : xt_a) & 1u, p.st, 108);
         if (X) ++xt_b; else ++xt_a;
-        return true;
+        tc_fence_after();
       };
       for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
-        const bool two = it.n_rows > sub_tokens;
         const int nt = walk.t1 - walk.t0;
-        for (int lt = 0; lt < nt && ok; ++lt, ++n) {
-          const uint32_t slot = n % SLOTS;
-          ok = mbar_wait_warp(kvbar(KFULL, slot), n / SLOTS & 1u, p.st, 111);
-          if (lt == 0)
-            for (uint32_t b = nq; b < nq + (two ? 2 : 1) && ok; ++b)
-              ok = mbar_wait_warp(bar(B_QFULL0 + (b & 1u)), b >> 1 & 1u, p.st, 110);
+        if (it.n_rows > sub_tokens) {
+          // two sub-tiles: per tile both chains' P V of the last and S of this
+          const uint32_t qa = nq & 1u, qb = qa ^ 1u;
+          nq += 2;
+          ok = fast_wait(kvbar(KFULL, n % SLOTS), n / SLOTS & 1u, p.st, 111);
+          ok = ok && fast_wait(bar(B_QFULL0 + qa), (nq - 2) >> 1 & 1u, p.st, 110) &&
+               fast_wait(bar(B_QFULL0 + qb), (nq - 1) >> 1 & 1u, p.st, 110);
           if (!ok) break;
-          const int x0 = two ? 0 : lt & 1, x1 = two ? 2 : x0 + 1;
+          tc_fence_after();
+          uint32_t slot = n % SLOTS;
+          if (leader) {
+            score(0, qa, slot);
+            score(1, qb, slot);
+            if (nt == 1) {
+              tc_commit(bar(B_QEMPTY0));
+              tc_commit(bar(B_QEMPTY0 + 1));
+            }
+            tc_commit(kvbar(KEMPTY, slot));
+          }
+          __syncwarp();
+          ++n;
 #pragma unroll 1
-          for (int X = x0; X < x1; ++X) {
-            uint32_t pend = X ? pend_b : pend_a;
-            if (pend && !(ok = issue_pv(X, pend))) break;
-            {
-              tc_fence_after();
-              const uint32_t qb = (nq + (two ? X : 0)) & 1u;
-              const uint32_t q = q_lo + qb * (NH * kHalf >> 4), k0 = k_lo + slot * (NH * kHalf >> 4);
-              if (leader) {
-#pragma unroll
-                for (int k = 0; k < HD / 16; ++k) {
-                  const uint32_t o = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
-                  tc_mma_f16(tmem + 128 * X, desc(q + o), desc(k0 + o), kIdescS, k > 0 ? 1u : 0u);
-                }
-                tc_commit(bar(B_SFULL0 + X));
+          for (int left = nt - 1; left > 0; --left, ++n) {
+            const uint32_t was = slot, more = left < nt - 1;
+            slot = n % SLOTS;
+            ok = fast_wait(kvbar(KFULL, slot), n / SLOTS & 1u, p.st, 111);
+            wait_p(0);
+            if (!ok) break;
+            if (leader) {
+              pv(0, was, more);
+              score(0, qa, slot);
+            }
+            __syncwarp();
+            wait_p(1);
+            if (!ok) break;
+            if (leader) {
+              pv(1, was, more);
+              tc_commit(kvbar(VEMPTY, was));
+              score(1, qb, slot);
+              tc_commit(kvbar(KEMPTY, slot));
+              if (left == 1) {
+                tc_commit(bar(B_QEMPTY0));
+                tc_commit(bar(B_QEMPTY0 + 1));
+              }
+            }
+            __syncwarp();
+          }
+          // the last P V of each, before anything waits for the next item's K
+          if (ok) wait_p(0);
+          if (ok && leader) {
+            pv(0, slot, nt > 1);
+            tc_commit(bar(B_OFULL0));
+          }
+          __syncwarp();
+          if (ok) wait_p(1);
+          if (ok && leader) {
+            pv(1, slot, nt > 1);
+            tc_commit(bar(B_OFULL0 + 1));
+            tc_commit(kvbar(VEMPTY, slot));
+          }
+          __syncwarp();
+        } else {
+          // one sub-tile: tile lt belongs to chain lt & 1
+          const uint32_t qb = nq & 1u;
+          ok = fast_wait(bar(B_QFULL0 + qb), nq >> 1 & 1u, p.st, 110);
+          ++nq;
+#pragma unroll 1
+          for (int lt = 0; lt < nt + 2 && ok; ++lt) {
+            const int X = lt & 1;
+            if (lt < nt) ok = fast_wait(kvbar(KFULL, n % SLOTS), n / SLOTS & 1u, p.st, 111);
+            const bool has_pv = lt >= 2 && lt - 2 < nt;
+            if (ok && has_pv) wait_p(X);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              if (has_pv) {  // of the chain's last tile, two before this one
+                const uint32_t was = (n - (lt < nt ? 2u : (uint32_t)(nt - (lt - 2)))) % SLOTS;
+                pv(X, was, lt >= 4);
+                if (lt >= nt) tc_commit(bar(B_OFULL0 + X));
+                tc_commit(kvbar(VEMPTY, was));
+              }
+              if (lt < nt) {
+                score(X, qb, n % SLOTS);
+                tc_commit(kvbar(KEMPTY, n % SLOTS));
                 if (lt == nt - 1) tc_commit(bar(B_QEMPTY0 + qb));
               }
-              __syncwarp();
-              const int step = two ? 1 : 2;
-              pend = 1u | (lt < step ? 2u : 0u) | (lt + step >= nt ? 4u : 0u) | (!two || X ? 8u : 0u) | slot << 8;
             }
-            if (X)
-              pend_b = pend;
-            else
-              pend_a = pend;
+            __syncwarp();
+            if (lt < nt) ++n;
           }
-          if (ok && leader) tc_commit(kvbar(KEMPTY, slot));
         }
-        nq += two ? 2 : 1;
-        // the item's last P V, before anything waits for the next item's K, the
-        // chain of the last tile last
-        const bool b_first = !two && (nt & 1);
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          const int X = b_first ? 1 - i : i;
-          const uint32_t pend = X ? pend_b : pend_a;
-          if (ok && pend) ok = issue_pv(X, pend);
-        }
-        pend_a = pend_b = 0;
       }
       // no tensor-core operation of this CTA may outlive its TMEM
       if (leader) tc_commit(bar(B_DRAIN));
