@@ -238,8 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
       float* dst = reinterpret_cast<float*>(a.o) + (int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD;
       const int64_t at_lse = (int64_t)(it.row0 + j) * a.n_q_heads + h;
       constexpr int kPart = kSlots * (HD + 2);
-      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
-      float* part = part_of(pl, kPart, cta, cta == c0);
+      float* part = part_of(pl, kPart, cta, walk.t0 == 0);
       if (act) {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a row that sees no key gives zeros
 #pragma unroll 1
@@ -272,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
       if (whole) continue;
       // ---- divided among CTAs: the last to arrive joins the parts, in CTA order
       __threadfence();
+      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
       join_sync();
       if (threadIdx.x == 0) {
         const int k = atomicAdd(&pl.arrived[walk.index], 1);
@@ -292,21 +292,23 @@ __global__ void __launch_bounds__(kThreads, 1) pages_attention_f32_kernel(PagesV
       }
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll 1
-      for (int k = 0; k < HD / 16; ++k) {
-        float4 acc[4] = {};
+      for (int k = 0; k < HD / 32; ++k) {
+        float4 acc[8] = {};
         for (int c = c0; c <= c1; ++c) {
-          const float w = fast_exp2(stat(c).x - base);
           const float* pc = part_of(pl, kPart, c, c == c0);
+          float4 v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pc) + (4 * k + i) * kSlots + r);
-            acc[i].x = fmaf(w, v.x, acc[i].x), acc[i].y = fmaf(w, v.y, acc[i].y);
-            acc[i].z = fmaf(w, v.z, acc[i].z), acc[i].w = fmaf(w, v.w, acc[i].w);
+          for (int i = 0; i < 8; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(pc) + (8 * k + i) * kSlots + r);
+          const float w = fast_exp2(stat(c).x - base);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[i].x = fmaf(w, v[i].x, acc[i].x), acc[i].y = fmaf(w, v[i].y, acc[i].y);
+            acc[i].z = fmaf(w, v[i].z, acc[i].z), acc[i].w = fmaf(w, v[i].w, acc[i].w);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<float4*>(dst)[4 * k + i] =
+        for (int i = 0; i < 8; ++i)
+          reinterpret_cast<float4*>(dst)[8 * k + i] =
               make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
       }
       if (a.lse) a.lse[at_lse] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);

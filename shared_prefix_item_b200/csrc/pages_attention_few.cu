@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // out, four elements to a thread; or, divided among CTAs, a part, and the
     // last CTA to arrive joins the parts in CTA order
     const bool whole = walk.whole(it);
-    const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
+    const int c0 = whole ? 0 : walk.first_cta(it), c1 = whole ? 0 : walk.last_cta(it);
     constexpr int kPart = kRows * (HD + 2), W4 = HD / 4;
     bool last = whole;
     if (!whole) {

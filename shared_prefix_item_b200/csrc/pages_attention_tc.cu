@@ -39,6 +39,8 @@
 #include "kernels.cuh"
 #include "pages.cuh"
 
+#include <type_traits>
+
 namespace duolm {
 
 namespace {
@@ -63,7 +65,7 @@ struct Lay {
   static constexpr int SMEM = STAT + 2048 + 1024;
 };
 
-enum { B_QFULL0, B_QFULL1, B_QEMPTY0, B_QEMPTY1, B_SFULL0, B_SFULL1, B_PFULL0, B_PFULL1, B_OFULL0, B_OFULL1, B_DRAIN, B_KV };
+enum { B_QFULL0, B_QFULL1, B_QEMPTY0, B_QEMPTY1, B_SFULL0, B_SFULL1, B_PHALF0, B_PHALF1, B_PVHALF0, B_PVHALF1, B_PFULL0, B_PFULL1, B_OFULL0, B_OFULL1, B_DRAIN, B_KV };
 // then per slot
 enum { KFULL, VFULL, KEMPTY, VEMPTY };
 template <int HD>
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
-    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), (i == B_PFULL0 || i == B_PFULL1) ? 4u + 1u : 1u);
+    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == B_PHALF0 || i == B_PHALF1 ? 4u + 1u : i == B_PFULL0 || i == B_PFULL1 ? 4u : 1u);
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -167,20 +169,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int lt = first; lt < nt; lt += step, ++n_xt) {
         ok = ok && mbar_wait_warp(bar(B_SFULL0 + X), n_xt & 1u, p.st, 100);
         if (!ok || !live) {
-          if (lane == 0) mbar_arrive(bar(B_PFULL0 + X));
+          if (lane == 0) {
+            mbar_arrive(bar(B_PHALF0 + X));
+            mbar_arrive(bar(B_PFULL0 + X));
+          }
           continue;
         }
         tc_fence_after();
         uint32_t sr[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, sr[c]);
+        tmem_ld32_async(tS, sr[0]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int i = 0; i < 32; ++i) tmem_ld_fence(sr[0][i]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) tmem_ld_fence(sr[c][i]);
+        for (int c = 1; c < 4; ++c) tmem_ld32_async(tS + 32 * c, sr[c]);
+        bool here = false;  // chunks 1 to 3
+        auto rest = [&]() {
+          if (here) return;
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 1; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) tmem_ld_fence(sr[c][i]);
+          here = true;
+        };
         const int n_vis = vis - (walk.t0 + lt) * kKeys;  // of this tile
         if (__any_sync(0xffffffffu, n_vis < kKeys)) {
+          rest();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             if (!__any_sync(0xffffffffu, n_vis < 32 * (c + 1))) continue;
@@ -189,44 +204,40 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (32 * c + i >= n_vis) sr[c][i] = __float_as_uint(-INFINITY);
           }
         }
-        // The weights go by the running maximum of the tiles before, and where
-        // their sum stays within 2^8 that stands: none is above 2^8 (P fits its
-        // type) and none that matters is lost.  Otherwise, in the first tile,
-        // and where the row has seen no key yet, the tile's maximum is taken and
-        // O and l are rescaled: decided for the whole warp, as the rescale is
-        // warp-collective, by its own rows alone (slots of no row hold what
-        // shared memory held).  The exponentials' instructions bound a chain,
-        // so the 64 of a maximum per tile count.
-        const float2 sv = make_float2(scale_log2, scale_log2);
-        float2 ls[2];
-        for (bool max_first = lt == first;; max_first = true) {
-          if (max_first) {
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // the maximum of m_used and the scores from chunk c0 on
+        auto max_from = [&](auto c0) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+          for (int c = decltype(c0)::value; c < 4; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                mx[(i >> 1) & 3] = fmax3f(mx[(i >> 1) & 3], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
-            const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2);
-            if (lt != first) {
-              const float corr = m_new == m_used ? 1.f : fast_exp2(m_used - m_new);
+            for (int i = 0; i < 32; i += 2)
+              mx[(i >> 1) & 3] = fmax3f(mx[(i >> 1) & 3], __uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1]));
+          return fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2);
+        };
+        // O, l and the sums so far go from m_used to m
+        auto rescale = [&](float m, float* sum) {
+          const float corr = m == m_used ? 1.f : fast_exp2(m_used - m);
 #pragma unroll 1
-              for (int c = 0; c < HD / 32; ++c) {
-                float v[32];
-                tmem_ld32(tO + 32 * c, v);
+          for (int c = 0; c < HD / 32; ++c) {
+            float v[32];
+            tmem_ld32(tO + 32 * c, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= corr;
-                tmem_st32(tO + 32 * c, v);
-              }
-              l *= corr;
-            }
-            m_used = m_new;
+            for (int i = 0; i < 32; ++i) v[i] *= corr;
+            tmem_st32(tO + 32 * c, v);
           }
+          l *= corr;
+          *sum *= corr;
+          m_used = m;
+        };
+        // P of half h (64 keys) over the first columns of S; its sum
+        const float2 sv = make_float2(scale_log2, scale_log2);
+        auto weights = [&](auto h) {
           const float nmu = m_used == -INFINITY ? 0.f : -m_used;  // no key of this row yet
           const float2 nv = make_float2(nmu, nmu);
-          ls[0] = ls[1] = make_float2(0.f, 0.f);
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 2 * decltype(h)::value; c < 2 * decltype(h)::value + 2; ++c) {
+            if (c == 1) rest();
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -238,14 +249,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16_async(tS + 16 * c, pk);
           }
           ls[0] = fadd2(ls[0], ls[1]);
-          if (max_first || !__any_sync(0xffffffffu, valid && (ls[0].x + ls[0].y > kSumLimit || (m_used == -INFINITY && n_vis > 0))))
-            break;
+          return ls[0].x + ls[0].y;
+        };
+        auto release = [&](int b) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(b));
+        };
+        // The weights go by the running maximum of the tiles before, and where
+        // the sum of 64 stays within 2^8 that stands: none is above 2^8 (P fits
+        // its type) and none that matters is lost.  Otherwise, in the first
+        // tile, and where the row has seen no key yet, the maximum is taken and
+        // O and l are rescaled: decided for the whole warp, as the rescale is
+        // warp-collective, by its own rows alone (slots of no row hold what
+        // shared memory held).  The 64 instructions of a maximum per tile are
+        // saved, and with P handed on by halves its P V begins while the
+        // second half's exponentials run.
+        float sum0, none = 0.f;
+        if (lt == first) {
+          rest();
+          m_used = max_from(std::integral_constant<int, 0>());
         }
-        l += ls[0].x + ls[0].y;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_PFULL0 + X));
+        for (bool again = lt == first;; again = true) {
+          sum0 = weights(std::integral_constant<int, 0>());
+          if (again || !__any_sync(0xffffffffu, valid && (sum0 > kSumLimit || (m_used == -INFINITY && n_vis > 0)))) break;
+          rescale(max_from(std::integral_constant<int, 0>()), &none);
+        }
+        release(B_PHALF0 + X);
+        float sum1;
+        for (bool again = lt == first;; again = true) {
+          sum1 = weights(std::integral_constant<int, 1>());
+          if (again || !__any_sync(0xffffffffu, valid && sum1 > kSumLimit)) break;
+          // the first half's P V has to be over
+          ok = mbar_wait_warp(bar(B_PVHALF0 + X), n_xt & 1u, p.st, 115);
+          tc_fence_after();
+          rescale(max_from(std::integral_constant<int, 2>()), &sum0);
+        }
+        release(B_PFULL0 + X);
+        l += sum0 + sum1;
       }
       // ---- the item's end.  O_X is overwritten only by the P V of the next
       // item's first P, which this warpgroup releases after reading it.
@@ -277,10 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool states = valid && (!joined || X == 0);  // writes the row's statistics
       float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a row that sees no key gives zeros
       char* dst = a.o + ((int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD) * 2;
-      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
       constexpr int kPart = 2 * kSub * (HD + 2), kRows = 2 * kSub;
       const int slot = (two ? X * kSub : 0) + r;
-      float* part = part_of(pl, kPart, cta, cta == c0);
+      float* part = part_of(pl, kPart, cta, walk.t0 == 0);
       const int col0 = joined && X == 1 ? HD / 64 : 0, col1 = joined && X == 0 ? HD / 64 : HD / 32;  // of 32
       const uint32_t tOA = joined ? tmem + lane_off + 256 : tO;
       if (act) {
@@ -327,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (joined) named_sync(2);  // each has read the other's O and statistics
       if (whole) continue;
       // ---- divided among CTAs: the last to arrive joins the parts, in CTA order
+      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
       __threadfence();
       named_sync(3);
       if (threadIdx.x == 0) {
@@ -348,24 +390,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll 1
-      for (int k = 2 * col0; k < 2 * col1; ++k) {
-        float4 acc[4] = {};
+      for (int k = col0; k < col1; ++k) {
+        float4 acc[8] = {};
+#pragma unroll 2
         for (int c = c0; c <= c1; ++c) {
           const float* pc = part_of(pl, kPart, c, c == c0);
+          float4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(pc) + (8 * k + i) * kRows + slot);
           const float w = fast_exp2(__ldcg(reinterpret_cast<const float2*>(pc + kRows * HD) + slot).x - base);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pc) + (4 * k + i) * kRows + slot);
-            acc[i].x += w * v.x, acc[i].y += w * v.y, acc[i].z += w * v.z, acc[i].w += w * v.w;
-          }
+          for (int i = 0; i < 8; ++i) acc[i].x += w * v[i].x, acc[i].y += w * v[i].y, acc[i].z += w * v[i].z, acc[i].w += w * v[i].w;
         }
-        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[2 * i] = pack2<BF16>(acc[i].x * inv, acc[i].y * inv);
-          w[2 * i + 1] = pack2<BF16>(acc[i].z * inv, acc[i].w * inv);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[2 * i] = pack2<BF16>(acc[4 * q + i].x * inv, acc[4 * q + i].y * inv);
+            w[2 * i + 1] = pack2<BF16>(acc[4 * q + i].z * inv, acc[4 * q + i].w * inv);
+          }
+          store32(dst + 64 * k + 32 * q, w, wide);
         }
-        store32(dst + 32 * k, w, wide);
       }
       if (states && a.lse)
         a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -460,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int X = 0; X < 2; ++X) {
             if (!two && X != ((t - walk.t0) & 1)) continue;
             // the phase before has to be over: this arrival belongs to the next
-            if (xt[X] > 0 && !(ok = mbar_wait_warp(bar(B_PFULL0 + X), (xt[X] - 1) & 1u, p.st, 114))) break;
-            if (lane == 0) mbar_arrive(bar(B_PFULL0 + X));
+            if (xt[X] > 0 && !(ok = mbar_wait_warp(bar(B_PHALF0 + X), (xt[X] - 1) & 1u, p.st, 114))) break;
+            if (lane == 0) mbar_arrive(bar(B_PHALF0 + X));
             ++xt[X];
           }
         }
@@ -475,10 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                      v_lo = ((sbase + L::V) >> 4) | (uint32_t)(kHalf >> 4) << 16;
       uint32_t n = 0, nq = 0, xt_a = 0, xt_b = 0;  // xt: P V issued
       bool ok = true;
-      auto pv = [&](int X, uint32_t slot, uint32_t accumulate) {
-        const uint32_t tS = tmem + 128 * X, tO = tmem + 256 + 128 * X, v = v_lo + slot * (NH * kHalf >> 4);
+      auto pv = [&](int X, uint32_t slot, int half, uint32_t accumulate) {
+        const uint32_t tS = tmem + 128 * X + 32 * half, tO = tmem + 256 + 128 * X;
+        const uint32_t v = v_lo + slot * (NH * kHalf >> 4) + half * (kKeys / 2 * 8);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k) tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? accumulate : 1u);
+        for (int k = 0; k < kKeys / 32; ++k) tc_mma_f16_ts(tO, tS + 8 * k, desc(v + k * 128), kIdescPV, k == 0 ? accumulate : 1u);
       };
       auto score = [&](int X, uint32_t qb, uint32_t slot) {
         const uint32_t q = q_lo + qb * (NH * kHalf >> 4), k0 = k_lo + slot * (NH * kHalf >> 4);
@@ -489,9 +536,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_commit(bar(B_SFULL0 + X));
       };
-      auto wait_p = [&](int X) {
-        ok = ok && fast_wait(bar(B_PFULL0 + X), (X ? xt_b : xt_a) & 1u, p.st, 108);
+      // P V of the first half when it is there, then P of the second
+      auto first_half = [&](int X, uint32_t slot, uint32_t accumulate) {
+        const uint32_t par = (X ? xt_b : xt_a) & 1u;
+        ok = ok && fast_wait(bar(B_PHALF0 + X), par, p.st, 108);
         if (X) ++xt_b; else ++xt_a;
+        if (!ok) return;
+        tc_fence_after();
+        if (leader) {
+          pv(X, slot, 0, accumulate);
+          tc_commit(bar(B_PVHALF0 + X));
+        }
+        __syncwarp();
+        ok = fast_wait(bar(B_PFULL0 + X), par, p.st, 109);
         tc_fence_after();
       };
       for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
@@ -522,17 +579,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t was = slot, more = left < nt - 1;
             slot = n % SLOTS;
             ok = fast_wait(kvbar(KFULL, slot), n / SLOTS & 1u, p.st, 111);
-            wait_p(0);
+            if (ok) first_half(0, was, more);
             if (!ok) break;
             if (leader) {
-              pv(0, was, more);
+              pv(0, was, 1, 1);
               score(0, qa, slot);
             }
             __syncwarp();
-            wait_p(1);
+            first_half(1, was, more);
             if (!ok) break;
             if (leader) {
-              pv(1, was, more);
+              pv(1, was, 1, 1);
               tc_commit(kvbar(VEMPTY, was));
               score(1, qb, slot);
               tc_commit(kvbar(KEMPTY, slot));
@@ -544,15 +601,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           // the last P V of each, before anything waits for the next item's K
-          if (ok) wait_p(0);
+          if (ok) first_half(0, slot, nt > 1);
           if (ok && leader) {
-            pv(0, slot, nt > 1);
+            pv(0, slot, 1, 1);
             tc_commit(bar(B_OFULL0));
           }
           __syncwarp();
-          if (ok) wait_p(1);
+          if (ok) first_half(1, slot, nt > 1);
           if (ok && leader) {
-            pv(1, slot, nt > 1);
+            pv(1, slot, 1, 1);
             tc_commit(bar(B_OFULL0 + 1));
             tc_commit(kvbar(VEMPTY, slot));
           }
@@ -566,14 +623,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int lt = 0; lt < nt + 2 && ok; ++lt) {
             const int X = lt & 1;
             if (lt < nt) ok = fast_wait(kvbar(KFULL, n % SLOTS), n / SLOTS & 1u, p.st, 111);
-            const bool has_pv = lt >= 2 && lt - 2 < nt;
-            if (ok && has_pv) wait_p(X);
+            const bool has_pv = lt >= 2 && lt - 2 < nt;  // of the chain's last tile, two before this one
+            const uint32_t was = (n - (lt < nt ? 2u : (uint32_t)(nt - (lt - 2)))) % SLOTS;
+            if (ok && has_pv) first_half(X, was, lt >= 4);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
-              if (has_pv) {  // of the chain's last tile, two before this one
-                const uint32_t was = (n - (lt < nt ? 2u : (uint32_t)(nt - (lt - 2)))) % SLOTS;
-                pv(X, was, lt >= 4);
+              if (has_pv) {
+                pv(X, was, 1, 1);
                 if (lt >= nt) tc_commit(bar(B_OFULL0 + X));
                 tc_commit(kvbar(VEMPTY, was));
               }
