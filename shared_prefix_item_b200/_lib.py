@@ -407,6 +407,9 @@ def _on(t, name: str, device: int):
 
 def _ints(t, name: str, device: int, shape=None) -> int:
     """Pointer of a contiguous int32 device array of this shape (None: any 1-D)."""
+    if (t.get_device() == device and _names.get(t.dtype) == "torch.int32" and t.is_contiguous()
+            and (t.dim() == 1 if shape is None else t.shape == shape)):
+        return t.data_ptr()
     _on(t, name, device)
     if _dtype_name(t) != "torch.int32" or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous int32 array is wanted")
@@ -512,11 +515,12 @@ class PagedBatch:
 
     def _rows(self, t, name: str, heads: int):
         """(pointer, row stride) of [n_rows, heads, head_dim] rows, or [n_rows, heads * head_dim]."""
-        c = self.cache
-        _on(t, name, c.device)
+        c, n = self.cache, self.n_rows
+        hd, st = c.head_dim, t.stride()
+        if t.get_device() != c.device:
+            _on(t, name, c.device)
         if t.dtype != c.dtype:
             raise ValueError(f"{name} of {t.dtype}, the cache of {c.dtype}")
-        n, hd, st = self.n_rows, c.head_dim, t.stride()
         if t.dim() == 3:
             good = t.shape == (n, heads, hd) and st[2] == 1 and (heads == 1 or st[1] == hd)
         else:
@@ -529,7 +533,11 @@ class PagedBatch:
     def _floats(self, t, name: str, shape) -> Optional[int]:
         if t is None:
             return None
-        _on(t, name, self.cache.device)
+        device = self.cache.device
+        if (t.get_device() == device and _names.get(t.dtype) == "torch.float32" and t.is_contiguous()
+                and (not shape or t.shape == shape)):
+            return t.data_ptr()
+        _on(t, name, device)
         if _dtype_name(t) != "torch.float32" or not t.is_contiguous() or (shape and t.shape != shape):
             raise ValueError(f"{name}: contiguous float32 {shape or ''} is wanted, got {t.dtype} {tuple(t.shape)}")
         return t.data_ptr()
