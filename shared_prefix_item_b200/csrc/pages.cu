@@ -5,8 +5,10 @@
 // ranks the free pages and writes what is to be done to the workspace.  The
 // others wait for its word, and then the whole grid does it: tables and
 // counts, a warp per sequence, and the page copies.  The decision needs a
-// prefix sum over all entries, the copies need every SM; a second launch
-// between them cost 2 us of the host's time and 1.5 us of the GPU's.
+// prefix sum over all entries, the copies need every SM; a second launch costs
+// the host 2 us.  Measured as a graph on one B200: free, fork and resize of four
+// sequences 13 us; of 256 through 28 layers 73 us, where the copied rows take 45
+// at the rate of a plain copy.
 #include "pages.cuh"
 
 #include <cstdarg>
@@ -89,6 +91,8 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 // turn 0 runs already and waits for nobody, so the others' wait ends whatever
 // order the CTAs start in.  Only the decider looks at the error flags: a CTA
 // that started late must not take an error of this call for an earlier one's.
+// (It is a chain of dependent loads, so the flags are loaded beside the entries
+// and tested at the decision's first barrier.)
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 8;
 enum : uint32_t { kWordNone = 0, kWordGo = 1, kWordStop = 2 };
@@ -96,9 +100,10 @@ enum : uint32_t { kWordNone = 0, kWordGo = 1, kWordStop = 2 };
 template <typename Decide>
 __device__ __forceinline__ bool decided(const PagesView& p, Decide decide) {
   __shared__ uint32_t s_word;
+  auto raised = [&] { return *reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0; };
   if (gridDim.x <= kCluster) {
     if (blockIdx.x == 0) {
-      const bool go = !pages_raised(p) && decide();
+      const bool go = decide(raised());
       __syncthreads();
       if (threadIdx.x == 0) s_word = go ? kWordGo : kWordStop;
       if (gridDim.x == 1) {
@@ -119,7 +124,7 @@ __device__ __forceinline__ bool decided(const PagesView& p, Decide decide) {
   if (threadIdx.x == 0) s_word = atomicAdd(&p.st->pad[0], 1u) & 0xffffu;
   __syncthreads();
   if (s_word == 0) {
-    const bool go = !pages_raised(p) && decide();
+    const bool go = decide(raised());
     __syncthreads();
     if (threadIdx.x == 0) {
       s_word = go ? kWordGo : kWordStop;
@@ -173,7 +178,8 @@ __device__ __forceinline__ PageCopy copy_of(const PagesWork& w, int64_t i) {
 // its own, so 16 warps have 128 KB on the way to every SM and no thread touches
 // the data.  HBM bound (read + write).  Pieces of 2 KB (ring of 6, 3 in flight)
 // measured 76.6 against 73.6 us for 256 forks through 28 layers, 1 KB 90.6,
-// 8 warps with rings of 6 x 4 KB 97.9; whole pages (compaction) 173 us in all.
+// 8 warps with rings of 6 x 4 KB 97.9.  Whole pages: 250 of 1,024 through 28
+// layers (932 MB read and written) 162 us in all, 5.8 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kPiece = 4096, kRing = 3, kDepth = 2;
 constexpr int kRingBytes = kWarps * kRing * kPiece;
@@ -269,17 +275,27 @@ __device__ __forceinline__ void init_bars(uint64_t* bars) {
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ bool resize_decide(const PagesView& p, const PagesWork& w, int n, const int32_t* __restrict__ seq,
                                               const int32_t* __restrict__ length, uint32_t* seen, int* s_scan,
-                                              uint32_t* s_err) {
+                                              uint32_t* s_err, bool raised) {
+  // the first entries, and whether the lowest pages are free, before anything waits
+  const bool mine = threadIdx.x < n;
+  const int seq0 = mine ? seq[threadIdx.x] : 0, len0 = mine && length ? length[threadIdx.x] : 0;
+  int low4 = 0;
+  if (length)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t id = 4ll * threadIdx.x + j;
+      if (id < p.n_pages && p.refs[id] == 0) low4 |= 1 << j;
+    }
   for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kThreads) seen[i] = 0;
   if (threadIdx.x == 0) *s_err = 0;
-  __syncthreads();
+  if (__syncthreads_or(raised)) return false;
   int64_t need_all = 0;
   int copies = 0;
   for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
     int need = 0, cow = 0, have = 0, want = 0;
     if (i < n) {
-      const int s = seq[i], len = length ? length[i] : 0;
+      const int s = i0 ? seq[i] : seq0, len = i0 ? (length ? length[i] : 0) : len0;
       if ((unsigned)s >= (unsigned)p.n_seqs || !claim(seen, s)) {
         atomicOr(s_err, ERR_BAD_SEQ);
       } else {
@@ -316,10 +332,13 @@ __device__ __forceinline__ bool resize_decide(const PagesView& p, const PagesWor
   int64_t found = 0;
   for (int64_t b = 0; !*s_err && found < need_all && b < p.n_pages; b += 4 * kThreads) {
     const int64_t id = b + 4 * threadIdx.x;
-    int free4 = 0;
+    int free4 = low4;
+    if (b > 0) {
+      free4 = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (id + j < p.n_pages && p.refs[id + j] == 0) free4 |= 1 << j;
+      for (int j = 0; j < 4; ++j)
+        if (id + j < p.n_pages && p.refs[id + j] == 0) free4 |= 1 << j;
+    }
     int all;
     int64_t at = found + block_scan<kThreads>(__popc(free4), s_scan, &all);
 #pragma unroll
@@ -364,7 +383,9 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(PagesView p, PagesWork
   pdl_launch_dependents();
   if (may_copy) init_bars(bars);
   pdl_wait();
-  const bool go = decided(p, [&] { return resize_decide(p, w, n, seq, length, reinterpret_cast<uint32_t*>(smem), s_scan, &s_err); });
+  const bool go = decided(p, [&](bool raised) {
+    return resize_decide(p, w, n, seq, length, reinterpret_cast<uint32_t*>(smem), s_scan, &s_err, raised);
+  });
   if (go) {
     const int lane = threadIdx.x & 31, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
     for (int i = warp; i < n; i += gridDim.x * kWarps) {
@@ -415,21 +436,23 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(PagesView p, int n, cons
   __shared__ uint32_t s_err;
   pdl_launch_dependents();
   pdl_wait();
-  const bool go = decided(p, [&] {
+  const bool go = decided(p, [&](bool raised) {
     for (int i = threadIdx.x; i < (p.n_seqs + 31) / 32; i += kThreads) seen[i] = 0;
     if (threadIdx.x == 0) s_err = 0;
-    __syncthreads();
+    if (__syncthreads_or(raised)) return false;
     for (int i = threadIdx.x; i < n; i += kThreads) {
-      const int d = dst[i];
-      if ((unsigned)d >= (unsigned)p.n_seqs || !claim(seen, d) || p.length[d] != 0) atomicOr(&s_err, ERR_BAD_SEQ);
+      const int d = dst[i], s = src[i], t = tokens[i];
+      const bool d_in = (unsigned)d < (unsigned)p.n_seqs, s_in = (unsigned)s < (unsigned)p.n_seqs;
+      const int d_len = d_in ? p.length[d] : 0, s_len = s_in ? p.length[s] : 0;
+      if (!d_in || !s_in || !claim(seen, d) || d_len != 0)
+        atomicOr(&s_err, ERR_BAD_SEQ);
+      else if (t < 0 || t > s_len || t > p.max_tokens())
+        atomicOr(&s_err, ERR_BAD_LENGTH);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads) {
-      const int s = src[i], t = tokens[i];
-      if ((unsigned)s >= (unsigned)p.n_seqs || (seen[s >> 5] >> (s & 31) & 1u))
-        atomicOr(&s_err, ERR_BAD_SEQ);
-      else if (t < 0 || t > p.length[s] || t > p.max_tokens())
-        atomicOr(&s_err, ERR_BAD_LENGTH);
+      const int s = src[i];
+      if ((unsigned)s < (unsigned)p.n_seqs && (seen[s >> 5] >> (s & 31) & 1u)) atomicOr(&s_err, ERR_BAD_SEQ);
     }
     __syncthreads();
     if (threadIdx.x == 0 && s_err) raise_error(p.st, s_err, 83);
@@ -517,7 +540,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(PagesView p, PagesWor
   pdl_launch_dependents();
   init_bars(bars);
   pdl_wait();
-  const bool go = decided(p, [&] {
+  const bool go = decided(p, [&](bool raised) {
+    if (__syncthreads_or(raised)) return false;
     compact_decide(p, w, live_out, s_scan);
     return true;
   });

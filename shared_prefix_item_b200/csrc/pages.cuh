@@ -43,12 +43,6 @@ struct PagesView {
   __host__ __device__ int max_tokens() const { return max_pages << page_shift; }
 };
 
-// Read once per kernel, after pdl_wait(), by every thread of the block:
-// the same answer in every thread of the block, whatever other blocks raise meanwhile
-__device__ __forceinline__ bool pages_raised(const PagesView& p) {
-  return __syncthreads_or(*reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0);
-}
-
 // ---- one CTA deciding for a whole call ----------------------------------------
 // Exclusive prefix sum over the block's NT values of 0..kScanCap; *total:
 // their sum, where that is below kScanCap, else kScanCap (callers refuse it).
@@ -263,9 +257,13 @@ struct ItemWalk {
 // the block): not while the cache's status is raised, not on a plan that such
 // a call was cut short on, and not on a buffer that holds no plan for these
 // sizes.
-__device__ __forceinline__ bool plan_usable(const PagesView& p, const PagesPlan& pl) {
+__device__ __forceinline__ bool plan_usable(const PagesView& p, const PagesPlan& pl, int cta = -1) {
   const bool raised = *reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0;
   const bool other = *reinterpret_cast<volatile const int*>(&pl.head->stale) != 0 || pl.head->key != pl.key;
+  if (cta >= 0) {  // the CTA's own records come into the L1 meanwhile
+    const int warm = pl.cta_item[cta] ^ pl.cta_first[cta].seq ^ pl.head->units;
+    asm volatile("" ::"r"(warm));
+  }
   if (!__syncthreads_or(raised || other)) return true;
   if (threadIdx.x == 0) {
     if (raised)

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kThreads, M == 16 && NC <= 4 ? 2 : 1)
   float* Ps = Vs + kTile * hd;
   pdl_launch_dependents();
   pdl_wait();
-  if (!plan_usable(p, pl)) return;
+  if (!plan_usable(p, pl, blockIdx.x)) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, cta = blockIdx.x;
   const float scale2 = a.scale * 1.4426950408889634f;

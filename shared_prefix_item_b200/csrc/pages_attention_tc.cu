@@ -2,10 +2,10 @@
 // tensor cores (16-bit elements).
 //
 // The softmax is one pass with a running maximum: for a tile of 128 keys
-// S = Q K^T, m' = max(m, max S), P = 2^(S - m'), l += sum P, O += P V, with O
-// (and l) rescaled by 2^(m - m') only when the maximum has grown by more than
-// 2^8; out = O / l.  S, O, m and l are fp32; P is rounded to the cache's type
-// because it is a tensor-core operand.
+// S = Q K^T, P = 2^(S - m), l += sum P, O += P V; out = O / l.  m is a maximum
+// of keys seen so far; it is taken anew, with O and l rescaled by 2^(m - m'),
+// only when the weights have outgrown 2^8.  S, O, m and l are fp32; P is rounded
+// to the cache's type because it is a tensor-core operand.
 //
 // An item (see the plan) is up to two sub-tiles of 128 (token, query head)
 // rows of one entry under one KV head, and a CTA has a range of its key
@@ -22,19 +22,28 @@
 //   warp 11   TMA of Q (one box of the entry's rows x the heads of the group; an
 //             item of one sub-tile leaves the other buffer for the next item's)
 //             and of V;
-//   warp 9    one lane issues tcgen05.mma, per tile first O_X += P_X V of the
-//             chain's previous tile (P read from tensor memory), then S_X;
-//   warp 10   relays arrivals: P_X counts as full when the softmax has stored it
+//   warp 9    an elected lane issues tcgen05.mma, per tile first O_X += P_X V of
+//             the chain's previous tile (P read from tensor memory, by halves),
+//             then S_X;
+//   warp 10   relays arrivals: P_X counts as there when the softmax has stored it
 //             and this warp has seen V of its tile, so that the issuing thread
-//             has one wait where it had two.  That thread bounds the kernel: a
-//             wait or commit costs it 100 to 200 cycles in which no product
-//             runs, eight products cost 512.  The warp also zeroes V rows behind
+//             has one wait where it had two.  The warp also zeroes V rows behind
 //             the last visible key: P is 0 there, but the slots may hold
 //             anything, and 0 x NaN is NaN.
-// Tensor memory: S/P of A in columns [0, 128), of B in [128, 256), O of A from
-// 256, of B from 384.  tcgen05.mma of one thread run in issue order, so S_X may
-// be issued right behind the P V that reads the same columns, and its commit
-// reports both.  Every mbarrier wait is bounded; a warp whose wait gives up
+// What bounds it: a step of both chains (256 rows x 128 keys) takes 3,250 cycles,
+// of which the products take about 2,600 (2,048 without their operands' share of
+// the shared memory's bandwidth) and each chain's softmax about 2,000, beside the
+// other chain's products; under sustained load the power limit.  Measured: four
+// chunks of 2,048 rows over 6,144 tokens 376 us in a burst, 442 sustained (1,040
+// and 880 TFLOP/s); candidates without a causal mask 340 and 405 us; 36 rows each
+// over 368 tokens 46 us (2.6 TB/s), bound by the few steps of an item and the
+// latencies around them.  Slower or no better: a polynomial for some of the
+// exponentials (+4 to 9%), K and V brought into L2 ahead of time (+20% on short
+// items), one code for both kinds of items.
+// Tensor memory: S and over it P of A in columns [0, 128), of B in [128, 256), O
+// of A from 256, of B from 384.  tcgen05.mma of one thread run in issue order, so
+// S_X may be issued right behind the P V that reads the same columns, and its
+// commit reports both.  Every mbarrier wait is bounded; a warp whose wait gives up
 // raises the status and goes on through the remaining barriers without work.
 #include "kernels.cuh"
 #include "pages.cuh"
@@ -140,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   pdl_wait();
-  const bool usable = plan_usable(p, pl);
+  const bool usable = plan_usable(p, pl, blockIdx.x);
   const int cta = blockIdx.x;
   PageItem it;
 
