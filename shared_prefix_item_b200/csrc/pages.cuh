@@ -154,8 +154,8 @@ enum PagesPath {
 struct PathShape {
   int slots;       // (token, query head) rows of one sub-tile
   int subs;        // sub-tiles of one item
-  int keys;        // keys of one tile
-  int grain;       // tiles of one unit in a batch of up to `few` tiles per CTA (else 1)
+  int keys;        // log2 of the keys of one tile
+  int grain;       // log2 of the tiles of one unit in a batch of up to `few` tiles per CTA (else 0)
   int few;
   int ctas_per_sm;
   int part_words;  // fp32 words of one partial result: subs x slots x (head_dim + 2)
@@ -178,7 +178,7 @@ constexpr int kRowOutside = -2;  // more rows than the sequence has tokens: nowh
 
 struct PlanHead {
   int n_items;
-  int units;  // of all items, each `grain` key tiles (an item's last may have fewer); CTA c of n takes
+  int units;  // of all items, each 2^grain key tiles (an item's last may have fewer); CTA c of n takes
               // [c units / n, (c + 1) units / n)
   int ctas;   // CTAs that take part: all, or one per unit where there are fewer
   int stale;  // a call on this plan was cut short: its counts of arrived parts are void
@@ -240,13 +240,13 @@ struct ItemWalk {
     *it = next_item;
     index = w.item++;
     const int end = min(it->unit0 + units_of(*it), w.end);
-    t0 = (w.unit - it->unit0) * w.grain;
-    t1 = min(it->n_tiles, (end - it->unit0) * w.grain);
+    t0 = (w.unit - it->unit0) << w.grain;
+    t1 = min(it->n_tiles, (end - it->unit0) << w.grain);
     w.unit = end;
     if (w.unit < w.end) next_item = items[w.item];
     return true;
   }
-  __device__ int units_of(const PageItem& it) const { return (it.n_tiles + w.grain - 1) / w.grain; }
+  __device__ int units_of(const PageItem& it) const { return (it.n_tiles + (1 << w.grain) - 1) >> w.grain; }
   // the CTAs that share the item
   __device__ int first_cta(const PageItem& it) const { return unit_cta(it.unit0, w.units, w.ctas); }
   __device__ int last_cta(const PageItem& it) const { return unit_cta(it.unit0 + units_of(it) - 1, w.units, w.ctas); }
@@ -266,9 +266,11 @@ __device__ __forceinline__ bool plan_usable(const PagesView& p, const PagesPlan&
   }
   if (!__syncthreads_or(raised || other)) return true;
   if (threadIdx.x == 0) {
-    if (raised)
+    // (a plan for other sizes is not this call's to mark, whichever CTA comes
+    // after the one that raised the status)
+    if (!other)
       pl.head->stale = 1;
-    else if (other)
+    else if (!raised)
       raise_error(p.st, ERR_STALE_PLAN, 89);
   }
   return false;

@@ -17,12 +17,12 @@ PathShape pages_path_shape(PagesPath path, int head_dim) {
   PathShape sh{};
   sh.slots = path == kPathSimt64 ? 64 : path == kPathTc || path == kPathF32 ? 128 : 16;
   sh.subs = path == kPathTc ? 2 : 1;
-  sh.keys = path == kPathTc ? 128 : 64;
+  sh.keys = path == kPathTc ? 7 : 6;
   // Joining an item that was divided costs about as much as 8 tiles of a few
   // rows (64 KB or less each) or 2 of a chunk; units of several tiles leave
   // fewer items divided, and less even work.  36 rows each of 64 sequences of
   // 404 tokens (14 tiles per CTA): 59 us with units of one tile, 52 with 4.
-  sh.grain = path == kPathTc ? 4 : 8;
+  sh.grain = path == kPathTc ? 2 : 3;
   sh.few = path == kPathTc ? 32 : 8;
   sh.ctas_per_sm = path == kPathFew || (path == kPathSimt16 && head_dim <= 128) ? 2 : 1;
   sh.part_words = sh.subs * sh.slots * (head_dim + 2);
@@ -91,7 +91,7 @@ __device__ __forceinline__ int item_keys(const BatchView& b, int rows, int len, 
   return b.causal ? max(0, len - rows + min(r0 + m, rows)) : len;
 }
 
-__device__ __forceinline__ int key_tiles(int n_keys, int keys) { return max(1, (n_keys + keys - 1) / keys); }  // one at least: an item that sees no key still writes its rows
+__device__ __forceinline__ int key_tiles(int n_keys, int keys) { return max(1, (n_keys + (1 << keys) - 1) >> keys); }  // one at least: an item that sees no key still writes its rows
 
 // The plan: the attention's items, how the CTAs divide their key tiles, and
 // where each query row's token lies in the cache.  Every CTA reads the entries
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   __shared__ int s_scan[3][32];
   __shared__ uint32_t s_err;
   __shared__ int4 s_entry[kPlanThreads];  // {sequence, first row, rows, length}
-  __shared__ int4 s_base[kPlanThreads];   // {items, units of one tile, units of `grain` tiles} of the entries before
+  __shared__ int4 s_base[kPlanThreads];   // {items, units of one tile, units of 2^grain tiles} of the entries before
   pdl_launch_dependents();
   const int tid = threadIdx.x;
   const bool near = b.n <= kPlanThreads, makes_items = near || blockIdx.x == 0;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
         for (int t = 0; t < tiles; ++t) {
           const int k = key_tiles(item_keys(b, rows, len, t * m, m), keys);
           u1 += k;
-          ug += (k + grain - 1) / grain;
+          ug += (k + (1 << grain) - 1) >> grain;
         }
         v[0] = tiles * p.n_kv_heads;
         v[1] = (int)min(u1 * p.n_kv_heads, (int64_t)kScanCap);
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
   // longer over them, but fewer items are divided and joined.
   const bool coarse = units[0] <= pl.ctas * few;
   const int total = coarse ? units[1] : units[0], ctas = min(pl.ctas, total);
-  if (!coarse) grain = 1;
+  if (!coarse) grain = 0;
   const bool refused = s_err || units[0] >= kScanCap || items > pl.max_items;
   if (blockIdx.x == 0 && tid == 0) {
     PlanHead& h = *pl.head;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
       const int first_unit = coarse ? here.z : here.y;
       const int end_unit = lo + 1 < b.n ? (coarse ? base[lo + 1].z : base[lo + 1].y) : total;
       const int tiles = (rows + m - 1) / m, h = (k - here.x) / tiles, t = (k - here.x) % tiles;
-      auto units_of = [&](int t2) { return (key_tiles(item_keys(b, rows, len, t2 * m, m), keys) + grain - 1) / grain; };
+      auto units_of = [&](int t2) { return (key_tiles(item_keys(b, rows, len, t2 * m, m), keys) + (1 << grain) - 1) >> grain; };
       int before = 0;
       if (b.causal)
         for (int t2 = 0; t2 < t; ++t2) before += units_of(t2);
