@@ -614,6 +614,52 @@ def test_attention_of_rows_aligned_to_16_bytes_alone(dt):
             assert bool(((out[off[i]:off[i + 1]].reshape(-1, 2, 64).double() - want).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("dt, layers", [("fp16", 24), ("fp32", 12)])
+def test_a_cache_whose_offsets_pass_32_bits(dt, layers):
+    """The last pages of the last layer: more than 2^32 bytes (and, in 16 bits,
+    2^31 elements) into K and V."""
+    torch = _t()
+    g = gen(51)
+    heads, hd, page, n_pages, group = 8, 128, 64, 2048, 2
+    c = Cache(dt, layers=layers, heads=heads, hd=hd, page=page, n_pages=n_pages, n_seqs=4, max_pages=n_pages)
+    c.resize([0], [2030 * page])  # takes the low pages; nothing is written there
+    c.resize([1], [300])
+    assert min(x for x in c.book.table[1] if x >= 0) == 2030
+    last = layers - 1
+    for x in (c.k, c.v):
+        for j in range(5):
+            m = min(page, 300 - page * j)
+            x[:, c.book.table[1][j], :, :m] = torch.randn((layers, heads, m, hd), generator=g, device="cuda").to(c.dt)
+    held = [x.clone() for x in c.kv(last, 1)]
+    c.fork([1], [2], [300])
+    c.resize([2], [304])  # a copy of the last page, in every layer
+    c.same()
+    for rows in (1, 4, 40):
+        new = max(0, rows - 4)
+        c.resize([2], [304 + new])
+        b, off, n = c.batch([2], [rows], heads * group)
+        q, k, v = (torch.randn((n, h, hd), generator=g, device="cuda").to(c.dt) for h in (heads * group, heads, heads))
+        out = torch.empty_like(q)
+        b.plan()
+        b.write(last, None, k, v, None)
+        if rows >= 4:  # (one row of the four that grew: the others are still NaN)
+            b.attention(last, q, out, None, hd ** -0.5)
+            K, V = c.kv(last, 2)
+            want, _, bound, _ = paged.attention(c.dt, q, K, V, hd ** -0.5, rows, 304 + new, True)
+            assert bool(((out.double() - want).abs() <= bound).all())
+        c.c.check()
+        K, V = c.kv(last, 2)
+        assert torch.equal(K[:, -rows:].transpose(0, 1), k) and torch.equal(V[:, -rows:].transpose(0, 1), v)
+        assert torch.equal(K[:, :300], held[0]) and torch.equal(V[:, :300], held[1])
+    c.free([0])
+    live = ints([0])
+    c.c.compact(c.table, c.refs, live)
+    assert c.book.compact()
+    c.same()
+    K, V = c.kv(last, 1)
+    assert torch.equal(K, held[0]) and torch.equal(V, held[1])
+
+
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("rows", [1, 64])
 def test_attention_of_more_tiles_than_are_taken_by_the_unit(dt, rows):
