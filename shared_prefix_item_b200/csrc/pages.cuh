@@ -188,8 +188,8 @@ struct PlanHead {
 };
 struct PagesPlan {
   PlanHead* head;
-  PageItem* cta_first;  // [ctas] item holding the CTA's first unit: which one, and the item itself
-  int32_t* cta_item;
+  PageItem* cta_first;  // [ctas] item holding the CTA's first unit
+  int4* cta_range;      // [ctas] {that item's index, the CTA's first unit, the one behind its last, 0}
   int32_t* arrived;   // [max_items] finished parts of a divided item (0 between calls)
   PageItem* items;    // [max_items]
   int4* base;         // [n] per entry: items and units before it (of more entries than one CTA holds)
@@ -219,10 +219,9 @@ struct CtaWork {  // a CTA's units [unit, end), the first of them in item `item`
   int unit, end, item, units, ctas, grain;
 };
 __device__ __forceinline__ CtaWork cta_work(const PagesPlan& pl, int cta) {
-  CtaWork w{0, 0, pl.cta_item[cta], pl.head->units, pl.head->ctas, pl.head->grain};
-  if (cta >= w.ctas) return w;
-  w.unit = cta_unit(cta, w.units, w.ctas);
-  w.end = cta_unit(cta + 1, w.units, w.ctas);
+  const int4 r = pl.cta_range[cta];
+  CtaWork w{r.y, r.z, r.x, pl.head->units, pl.head->ctas, pl.head->grain};
+  if (cta >= w.ctas) w.unit = w.end = 0;
   return w;
 }
 // A CTA's items in order, the next one's record already on its way.  Every
@@ -261,7 +260,7 @@ __device__ __forceinline__ bool plan_usable(const PagesView& p, const PagesPlan&
   const bool raised = *reinterpret_cast<volatile const uint32_t*>(&p.st->flags) != 0;
   const bool other = *reinterpret_cast<volatile const int*>(&pl.head->stale) != 0 || pl.head->key != pl.key;
   if (cta >= 0) {  // the CTA's own records come into the L1 meanwhile
-    const int warm = pl.cta_item[cta] ^ pl.cta_first[cta].seq ^ pl.head->units;
+    const int warm = pl.cta_range[cta].x ^ pl.cta_first[cta].seq ^ pl.head->units;
     asm volatile("" ::"r"(warm));
   }
   if (!__syncthreads_or(raised || other)) return true;

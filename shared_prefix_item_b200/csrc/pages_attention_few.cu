@@ -7,18 +7,21 @@
 // O' = O 2^(m - m') + P V; S, m, l and O in fp32, P rounded to the cache's
 // type because it is a matrix operand.
 //
-// A tile is 64 keys.  One warp fetches tiles with TMA (a lane to each
-// 64-element box of a page, 128-byte swizzle), four warps each take 16 of the
-// tile's keys with statistics and O of their own, joined when the item ends:
-// no barrier between the four inside an item.  16 rows are half of the
-// smallest tcgen05 tile's quarter, and S and P would go through tensor memory
-// between two products of a few hundred cycles; mma.sync (m16n8k16) keeps them
-// in registers and needs a tenth of the time the tile's bytes take to arrive.
-// Two CTAs per SM, each with 96 KB of tiles in flight or in use, so that one
-// CTA's item ends are covered by the other's loads.  Measured: one token of each
-// of 64 sequences of 16,000 (4.3 GB of K and V) 657 us, 6.6 TB/s; pages of 8
-// tokens 5.9 TB/s.  A short call (one token over 300) is a chain of latencies,
-// about 7 us.
+// A tile is 64 keys; each of four warps takes 16 of them, with statistics and O
+// of its own, joined when the item ends, and with a ring of its own that it
+// fills by TMA (a lane to each page, both halves of head_dim in one box,
+// 128-byte swizzle): a slot that has been read is refilled at once, into the
+// CTA's next item where the item's tiles are all on the way, and no warp waits
+// for another inside an item.  16 rows are half of the smallest tcgen05 tile's
+// quarter, and S and P would go through tensor memory between two products of a
+// few hundred cycles; mma.sync (m16n8k16) keeps them in registers and needs a
+// tenth of the time the tile's bytes take to arrive.  Two CTAs per SM, each with
+// 96 KB of tiles in flight or in use, so that one CTA's item ends are covered by
+// the other's loads.  Measured: one token of each of 64 sequences of 16,000 (4.3
+// GB of K and V) 665 us, 6.5 TB/s, with pages of 8 tokens 6.2; one token over 300
+// 7.5 us, a chain of latencies.  One loading warp for all four, with larger boxes
+// and a barrier per tile, took 650 us for the former (5.9 TB/s with pages of 8)
+// and 9.8 for the latter.
 #include "kernels.cuh"
 #include "pages.cuh"
 
@@ -27,21 +30,20 @@ namespace duolm {
 namespace {
 
 constexpr int kTile = 64, kRows = 16;
-constexpr int kMathWarps = 4, kMath = 32 * kMathWarps, kThreads = kMath + 32;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kOwn = kTile / kWarps;  // a warp's keys of a tile
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int HD>
 struct Lay {
-  static constexpr int NH = HD / 64;               // 64-element halves of a row
-  static constexpr int HALF = kTile * 128;         // one half of a tile's K (or V)
-  static constexpr int STAGE = 2 * NH * HALF;      // K, then V
-  static constexpr int STAGES = 96 * 1024 / STAGE; // 3 (head_dim 128) or 6
-  static constexpr int LD = HD + 8;                // row of the joined O: 8 banks on per row
-  static constexpr int ACC = STAGES * STAGE, STAT = ACC + kRows * LD * 4, BAR = STAT + kMathWarps * kRows * 8;
-  static constexpr int SMEM = BAR + 16 * STAGES + 16 + 1024;
+  static constexpr int NH = HD / 64;                   // 64-element halves of a row
+  static constexpr int HALF = kOwn * 128;              // one half of a warp's keys
+  static constexpr int STAGE = 2 * NH * HALF;          // K, then V
+  static constexpr int STAGES = 24 * 1024 / STAGE;     // of a warp: 3 (head_dim 128) or 6
+  static constexpr int LD = HD + 8;                    // row of the joined O: 8 banks on per row
+  static constexpr int ACC = kWarps * STAGES * STAGE;  // float [warp][4][LD]
+  static constexpr int STAT = ACC + kWarps * 4 * LD * 4, BAR = STAT + kWarps * kRows * 8;
+  static constexpr int SMEM = BAR + 8 * kWarps * STAGES + 16 + 1024;
 };
-
-__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -82,82 +84,95 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int NH = L::NH, STAGES = L::STAGES, NT = HD / 8;  // NT: 8-column tiles of O
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bars = sbase + L::BAR;
-  auto full = [&](uint32_t s) { return bars + 16 * s; };
-  auto empty = [&](uint32_t s) { return bars + 16 * s + 8; };
-  int* s_last = reinterpret_cast<int*>(smem + L::BAR + 16 * STAGES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * L::STAGE, bars = smem_u32(smem) + L::BAR + warp * STAGES * 8;
+  int* s_last = reinterpret_cast<int*>(smem + L::BAR + 8 * kWarps * STAGES);
   float* acc = reinterpret_cast<float*>(smem + L::ACC);
   float2* stat = reinterpret_cast<float2*>(smem + L::STAT);  // [warp][row] m, l
 
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == kMathWarps && lane == 0) {
-    prefetch_tensormap(&tmK);
-    prefetch_tensormap(&tmV);
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kMathWarps);
+  if (lane == 0) {
+    if (warp == 0) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
     }
+    for (int s = 0; s < STAGES; ++s) mbar_init(bars + 8 * s, 1);
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait();
   if (!plan_usable(p, pl, blockIdx.x)) return;
   const int cta = blockIdx.x, G = a.group;
-  PageItem it;
 
-  if (warp == kMathWarps) {
-    // ---- TMA
-    const int box = min(p.page_tokens, kTile), boxes = kTile / box * NH;
-    const int bj = lane / NH, bh = lane % NH;
-    uint32_t n = 0;
-    bool ok = true;
-    for (ItemWalk walk(pl, cta); ok && walk.next(&it);) {
-      const int32_t* table = p.table + (int64_t)it.seq * p.max_pages;
-      auto fetch = [&](int t) {
-        const int key = t * kTile + bj * box;
-        return lane < boxes && key < it.n_keys ? table[key >> p.page_shift] : -1;
-      };
-      int id = fetch(walk.t0);
-      for (int t = walk.t0; t < walk.t1; ++t, ++n) {
-        const uint32_t slot = n % STAGES;
-        const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
-        const int left = it.n_keys - t * kTile;
-        const int n_boxes = left <= 0 ? 0 : min(kTile / box, (left + box - 1) / box) * NH;
-        const bool have = lane < n_boxes;
-        if (have && (unsigned)id >= (unsigned)p.n_pages) {
-          raise_on_plan(p, pl, ERR_BAD_INDEX, 120);
-          id = 0;
-        }
-        const int y = have ? ((id * p.n_kv_heads + it.kv_head) << p.page_shift) + ((t * kTile + bj * box) & (p.page_tokens - 1))
-                           : 0;
-        const uint32_t dst = sbase + slot * L::STAGE + bh * L::HALF + bj * box * 128;
-        if (!(ok = mbar_wait_warp(empty(slot), (n / STAGES & 1u) ^ 1u, p.st, 121))) break;
-        if (lane == 0) mbar_arrive_expect_tx(full(slot), 2 * n_boxes * box * 128);
-        __syncwarp();
-        if (have) {
-          tma_load_2d(&tmK, dst, full(slot), bh * 64, y);
-          tma_load_2d(&tmV, dst + NH * L::HALF, full(slot), bh * 64, y);
-        }
-        id = next_id;
-      }
+  // ---- loads.  The cursor: the next tile to fetch, of the item at hand or
+  // (c_next) of the one behind it, that item's end, table, keys and KV head.
+  // Lane 2 j + v fetches K (v = 0) or V (1) of box j of the warp's keys; c_id is
+  // the page that it lies in.
+  const int box_shift = min(p.page_shift, 4), box = 1 << box_shift, n_box = kOwn >> box_shift, chunk = NH * box * 128;
+  static_assert(kOwn == 16, "box_shift");
+  PageItem it;
+  ItemWalk walk(pl, cta);
+  bool have = walk.next(&it);
+  uint32_t n = 0, m_issued = 0;  // tiles read, tiles fetched
+  bool c_next = false, c_ok = false;
+  int c_t = walk.t0, c_end = walk.t1, c_keys = it.n_keys, c_head = it.kv_head, c_id = -1;
+  const int32_t* c_table = p.table + (int64_t)it.seq * p.max_pages;
+  auto page_of = [&](int t, int j) {
+    const int key = t * kTile + warp * kOwn + j * box;
+    return key < c_keys ? c_table[key >> p.page_shift] : -1;
+  };
+  auto seek = [&]() {
+    if (c_t >= c_end && !c_next && walk.w.unit < walk.w.end) {
+      const PageItem& x = walk.next_item;
+      c_next = true;
+      c_t = 0;
+      c_end = min(x.n_tiles, (min(x.unit0 + walk.units_of(x), walk.w.end) - x.unit0) << walk.w.grain);
+      c_keys = x.n_keys;
+      c_head = x.kv_head;
+      c_table = p.table + (int64_t)x.seq * p.max_pages;
     }
-    // leave no copy in flight into shared memory that this CTA gives up
-    if (!ok)
-      for (uint32_t k = n > STAGES ? n - STAGES : 0; k < n; ++k) mbar_wait_warp(full(k % STAGES), k / STAGES & 1u, p.st, 122);
-    return;
+    c_ok = c_t < c_end;
+    if (c_ok && lane < 2 * n_box) c_id = page_of(c_t, lane >> 1);
+  };
+  const CUtensorMap* map = lane & 1 ? &tmV : &tmK;
+  const uint32_t lane_dst = ring + (lane & 1) * NH * L::HALF + (lane >> 1) * chunk;
+  auto issue = [&](int id) {
+    const uint32_t slot = m_issued % STAGES, b = bars + 8 * slot;
+    const int k0 = c_t * kTile + warp * kOwn, left = c_keys - k0;  // the warp's keys
+    const int boxes = left <= 0 ? 0 : min(n_box, (left + box - 1) >> box_shift);
+    const bool mine = lane < 2 * boxes;
+    if (mine && (unsigned)id >= (unsigned)p.n_pages) {
+      raise_on_plan(p, pl, ERR_BAD_INDEX, 120);
+      id = 0;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(b, 2 * boxes * chunk);
+    __syncwarp();
+    if (mine)
+      tma_load_3d(map, lane_dst + slot * L::STAGE, b, 0,
+                  ((id * p.n_kv_heads + c_head) << p.page_shift) + ((k0 + (lane >> 1) * box) & (p.page_tokens - 1)), 0);
+    ++m_issued;
+    ++c_t;
+  };
+  if (have) {
+    // the first tiles' pages in one look
+    const int per = 2 * n_box, s = lane >> (5 - box_shift);  // (per = 2^(5 - box_shift))
+    const int first = s < STAGES && c_t + s < c_end ? page_of(c_t + s, (lane & (per - 1)) >> 1) : -1;
+    for (int k = 0; k < STAGES && c_t < c_end; ++k) issue(__shfl_sync(0xffffffffu, first, k * per + (lane & (per - 1))));
+    seek();
   }
 
-  // ---- math warps: keys [16 warp, 16 warp + 16) of every tile
+  // ---- keys [16 warp, 16 warp + 16) of every tile
   const int g = lane >> 2, c2 = (lane & 3) * 2;
   const float scale_log2 = a.scale * 1.4426950408889634f;
   // lane's row of the four 8 x 8 matrices that one ldmatrix reads
-  const int k_key = warp * 16 + (lane >> 4) * 8 + (lane & 7), k_chunk = lane >> 3 & 1;
-  const int v_key = warp * 16 + (lane >> 3 & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
-  uint32_t n = 0;
+  const int k_key = (lane >> 4) * 8 + (lane & 7), k_chunk = lane >> 3 & 1;
+  const int v_key = (lane >> 3 & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
+  const uint32_t half = box * 128;  // a box's second half lies behind its first
+  const uint32_t k_off = (k_key >> box_shift) * chunk + (k_key & (box - 1)) * 128,
+                 v_off = (v_key >> box_shift) * chunk + (v_key & (box - 1)) * 128;
   bool ok = true;
-  for (ItemWalk walk(pl, cta); walk.next(&it);) {
+  uint32_t lost = 0;  // where a wait gave up
+  while (have) {
     const int rows = min(kRows, it.n_rows * G);
     // Q as the products' first operand: rows g and g + 8, elements 16 k + c2.. and 16 k + 8 + c2..
     uint32_t qf[HD / 16][4];
@@ -179,16 +194,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     for (int t = walk.t0; t < walk.t1; ++t, ++n) {
       const uint32_t slot = n % STAGES;
-      ok = ok && mbar_wait_warp(full(slot), n / STAGES & 1u, p.st, 123);
+      if (ok && !(ok = mbar_wait_warp(bars + 8 * slot, n / STAGES & 1u, p.st, 123))) lost = n;
       if (!ok) continue;
-      const int k0 = t * kTile + warp * 16;
+      const int k0 = t * kTile + warp * kOwn;
       if (k0 < it.n_keys) {
-        const uint32_t kb = sbase + slot * L::STAGE + k_key * 128, vb = sbase + slot * L::STAGE + NH * L::HALF + v_key * 128;
+        const uint32_t kb = ring + slot * L::STAGE + k_off, vb = ring + slot * L::STAGE + NH * L::HALF + v_off;
         float s[4][4] = {};  // two chains per 8 keys, so that the products do not wait on one another
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
           uint32_t kf[4];
-          ldsm4(kf, kb + (k >> 2) * L::HALF + ((((k & 3) * 2 + k_chunk) ^ (k_key & 7)) << 4));
+          ldsm4(kf, kb + (k >> 2) * half + ((((k & 3) * 2 + k_chunk) ^ (k_key & 7)) << 4));
           mma16<BF16>(s[(k & 1) * 2], qf[k], kf[0], kf[1]);
           mma16<BF16>(s[(k & 1) * 2 + 1], qf[k], kf[2], kf[3]);
         }
@@ -234,98 +249,98 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c) {
           uint32_t vf[4];
-          ldsm4_t(vf, vb + (c >> 2) * L::HALF + ((((c & 3) * 2 + v_chunk) ^ (v_key & 7)) << 4));
+          ldsm4_t(vf, vb + (c >> 2) * half + ((((c & 3) * 2 + v_chunk) ^ (v_key & 7)) << 4));
           mma16<BF16>(o[2 * c], pf, vf[0] & lo, vf[1] & hi);
           mma16<BF16>(o[2 * c + 1], pf, vf[2] & lo, vf[3] & hi);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(slot));
+      __syncwarp();  // every lane has read the slot
+      while (c_ok && m_issued - n <= STAGES) {
+        issue(c_id);
+        seek();
+      }
     }
-    // ---- the item's end: the four warps' parts joined, one after the other
+    // ---- the item's end: the four warps' parts joined, four rows at a time, an
+    // element (four columns of a row) to a thread, in warp order
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if ((lane & 3) == 0) stat[warp * kRows + g + 8 * i] = make_float2(m[i], l[i]);
     }
-    math_sync();
-    float wt[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kMathWarps; ++w) mm = fmaxf(mm, stat[w * kRows + g + 8 * i].x);
-      wt[i] = fast_exp2(m[i] - (mm == -INFINITY ? 0.f : mm));
-    }
-#pragma unroll 1
-    for (int w = 0; w < kMathWarps; ++w) {
-      if (w == warp)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (g + 8 * i < rows)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              float2* dst = reinterpret_cast<float2*>(acc + (g + 8 * i) * L::LD + t * 8 + c2);
-              float2 x = w ? *dst : make_float2(0.f, 0.f);
-              x.x = fmaf(o[t][2 * i], wt[i], x.x);
-              x.y = fmaf(o[t][2 * i + 1], wt[i], x.y);
-              *dst = x;
-            }
-      math_sync();
-    }
-    // out, four elements to a thread; or, divided among CTAs, a part, and the
-    // last CTA to arrive joins the parts in CTA order
     const bool whole = walk.whole(it);
-    const int c0 = whole ? 0 : walk.first_cta(it), c1 = whole ? 0 : walk.last_cta(it);
     constexpr int kPart = kRows * (HD + 2), W4 = HD / 4;
-    bool last = whole;
-    if (!whole) {
-      float* part = part_of(pl, kPart, cta, cta == c0);
-      for (int e = threadIdx.x; e < rows * W4; e += kMath) {
-        const int r = e / W4, c = e % W4;
-        __stcg(reinterpret_cast<float4*>(part) + e, *reinterpret_cast<const float4*>(acc + r * L::LD + 4 * c));
-      }
-      if (threadIdx.x < rows) {
+    float* part = part_of(pl, kPart, cta, walk.t0 == 0);
+    // out of the sums x (of row r, columns 4 c) over weights that sum to ll
+    auto store = [&](int r, int c, const float4& x, float mm, float ll) {
+      const int j = r / G, h = it.kv_head * G + r % G;
+      const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // a row that sees no key gives zeros
+      *reinterpret_cast<uint2*>(a.o + ((int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD + 4 * c) * 2) =
+          make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
+      if (a.lse && c == 0)
+        a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = mm == -INFINITY ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    };
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (4 * q >= rows) break;
+      if ((g >> 2) == (q & 1))
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          *reinterpret_cast<float2*>(acc + (warp * 4 + (g & 3)) * L::LD + t * 8 + c2) =
+              make_float2(o[t][2 * (q >> 1)], o[t][2 * (q >> 1) + 1]);
+      __syncthreads();
+      const int r = 4 * q + threadIdx.x / W4, c = threadIdx.x % W4;
+      if (threadIdx.x < 4 * W4 && r < rows) {
         float mm = -INFINITY, ll = 0.f;
-        for (int w = 0; w < kMathWarps; ++w) mm = fmaxf(mm, stat[w * kRows + threadIdx.x].x);
-        for (int w = 0; w < kMathWarps; ++w) {
-          const float2 s = stat[w * kRows + threadIdx.x];
-          ll += s.y * fast_exp2(s.x - (mm == -INFINITY ? 0.f : mm));
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * kRows + r].x);
+        const float base = mm == -INFINITY ? 0.f : mm;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 s = stat[w * kRows + r];
+          const float wt = fast_exp2(s.x - base);
+          const float4 y = *reinterpret_cast<const float4*>(acc + (w * 4 + (r & 3)) * L::LD + 4 * c);
+          ll = fmaf(s.y, wt, ll);
+          x.x = fmaf(y.x, wt, x.x);
+          x.y = fmaf(y.y, wt, x.y);
+          x.z = fmaf(y.z, wt, x.z);
+          x.w = fmaf(y.w, wt, x.w);
         }
-        __stcg(reinterpret_cast<float2*>(part + kRows * HD) + threadIdx.x, make_float2(mm, ll));
+        if (whole) {
+          if (ok) store(r, c, x, mm, ll);
+        } else {
+          __stcg(reinterpret_cast<float4*>(part) + r * W4 + c, x);
+          if (c == 0) __stcg(reinterpret_cast<float2*>(part + kRows * HD) + r, make_float2(mm, ll));
+        }
       }
+      __syncthreads();  // acc and stat are read
+    }
+    if (!whole) {
+      // divided among CTAs: the last to arrive joins the parts, in CTA order
       __threadfence();
-      math_sync();
+      __syncthreads();
+      const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
       if (threadIdx.x == 0) {
         const int k = atomicAdd(&pl.arrived[walk.index], 1);
         *s_last = k == c1 - c0;
         if (*s_last) pl.arrived[walk.index] = 0;
       }
-      math_sync();
-      last = *s_last;
-      __threadfence();
-    }
-    if (last && ok) {
-      const int n_parts = whole ? kMathWarps : c1 - c0 + 1;
-      auto part = [&](int k) { return part_of(pl, kPart, c0 + k, k == 0); };
-      for (int e = threadIdx.x; e < rows * W4; e += kMath) {
-        const int r = e / W4, c = e % W4, j = r / G, h = it.kv_head * G + r % G;
-        auto stat_of = [&](int k) {
-          return whole ? stat[k * kRows + r] : __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * HD) + r);
-        };
-        float mm = -INFINITY, ll = 0.f;
-        for (int k = 0; k < n_parts; ++k) mm = fmaxf(mm, stat_of(k).x);
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (whole) {
-          for (int k = 0; k < n_parts; ++k) ll += stat_of(k).y * fast_exp2(stat_of(k).x - base);
-          x = *reinterpret_cast<const float4*>(acc + r * L::LD + 4 * c);
-        } else {
+      __syncthreads();
+      if (*s_last && ok) {
+        __threadfence();
+        for (int e = threadIdx.x; e < rows * W4; e += kThreads) {
+          const int r = e / W4;
+          auto stat_of = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(part_of(pl, kPart, c, c == c0) + kRows * HD) + r); };
+          float mm = -INFINITY, ll = 0.f;
 #pragma unroll 8
-          for (int k = 0; k < n_parts; ++k) {
-            const float2 s = stat_of(k);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(part(k)) + e);
+          for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, stat_of(c).x);
+          const float base = mm == -INFINITY ? 0.f : mm;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int c = c0; c <= c1; ++c) {
+            const float2 s = stat_of(c);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(pl, kPart, c, c == c0)) + e);
             const float w = fast_exp2(s.x - base);
             ll = fmaf(s.y, w, ll);
             x.x = fmaf(y.x, w, x.x);
@@ -333,17 +348,26 @@ __global__ void __launch_bounds__(kThreads, 2)
             x.z = fmaf(y.z, w, x.z);
             x.w = fmaf(y.w, w, x.w);
           }
+          store(r, e % W4, x, mm, ll);
         }
-        const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // a row that sees no key gives zeros
-        *reinterpret_cast<uint2*>(a.o + ((int64_t)(it.row0 + j) * a.o_stride + (int64_t)h * HD + 4 * c) * 2) =
-            make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
-        if (a.lse && c == 0)
-          a.lse[(int64_t)(it.row0 + j) * a.n_q_heads + h] = mm == -INFINITY ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      }
+      // (the flag is next written behind two of the next item's barriers)
+    }
+    have = walk.next(&it);
+    if (have && ok) {
+      c_next = false;  // the cursor has been in this item since its last tile was on the way
+      seek();
+      while (c_ok && m_issued - n < STAGES) {
+        issue(c_id);
+        seek();
       }
     }
-    math_sync();  // acc and stat are read before the next item's
   }
-  if (!ok && lane == 0) pl.head->stale = 1;
+  if (!ok) {
+    if (lane == 0) pl.head->stale = 1;
+    // leave no copy in flight into shared memory that this CTA gives up
+    for (uint32_t k = lost + 1; k < m_issued; ++k) mbar_wait_warp(bars + 8 * (k % STAGES), k / STAGES & 1u, p.st, 122);
+  }
 }
 
 namespace {
@@ -365,10 +389,13 @@ cudaError_t pages_attention_few(const PagesView& p, const PagesPlan& pl, const A
   CUtensorMap tk, tv;
   char err[128];
   const uint64_t rows = (uint64_t)p.n_pages * p.n_kv_heads * p.page_tokens;
-  const uint32_t box = std::min(p.page_tokens, kTile);
+  const uint32_t box = std::min(p.page_tokens, kOwn);
   const int64_t off = a.layer * p.layer_bytes();
-  if (!make_tmap_f16_2d(&tk, p.k + off, p.head_dim, rows, 64, box, err, sizeof err) ||
-      !make_tmap_f16_2d(&tv, p.v + off, p.head_dim, rows, 64, box, err, sizeof err))
+  // {64 elements, cache rows, halves of head_dim}
+  const uint64_t dims[3] = {64, rows, (uint64_t)p.head_dim / 64}, strides[2] = {(uint64_t)p.head_dim * 2, 128};
+  const uint32_t boxes[3] = {64, box, (uint32_t)p.head_dim / 64};
+  if (!make_tmap_f16_3d(&tk, p.k + off, dims, strides, boxes, err, sizeof err) ||
+      !make_tmap_f16_3d(&tv, p.v + off, dims, strides, boxes, err, sizeof err))
     return cudaErrorInvalidValue;
   if (p.head_dim == 128) return bf16 ? launch_few<128, true>(tk, tv, p, pl, a, s) : launch_few<128, false>(tk, tv, p, pl, a, s);
   return bf16 ? launch_few<64, true>(tk, tv, p, pl, a, s) : launch_few<64, false>(tk, tv, p, pl, a, s);

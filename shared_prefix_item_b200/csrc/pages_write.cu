@@ -43,7 +43,7 @@ int64_t pages_plan_layout(char* base, int64_t n, int64_t n_rows, int n_kv_heads,
   PagesPlan pl;
   pl.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
   pl.cta_first = reinterpret_cast<PageItem*>(take((int64_t)sizeof(PageItem) * ctas));
-  pl.cta_item = reinterpret_cast<int32_t*>(take(4 * ctas));
+  pl.cta_range = reinterpret_cast<int4*>(take(16 * ctas));
   pl.arrived = reinterpret_cast<int32_t*>(take(4 * max_items));
   pl.items = reinterpret_cast<PageItem*>(take((int64_t)sizeof(PageItem) * max_items));
   pl.base = reinterpret_cast<int4*>(take(16 * n));
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(PagesView p, B
         const int first = cta_unit(c, total, ctas);
         if (first >= end) break;
         if (first < it.unit0) continue;
-        pl.cta_item[c] = k;
+        pl.cta_range[c] = make_int4(k, first, cta_unit(c + 1, total, ctas), 0);
         pl.cta_first[c] = it;
       }
     }
