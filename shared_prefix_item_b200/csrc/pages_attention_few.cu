@@ -7,21 +7,20 @@
 // O' = O 2^(m - m') + P V; S, m, l and O in fp32, P rounded to the cache's
 // type because it is a matrix operand.
 //
-// A tile is 64 keys; each of four warps takes 16 of them, with statistics and O
-// of its own, joined when the item ends, and with a ring of its own that it
-// fills by TMA (a lane to each page, both halves of head_dim in one box,
-// 128-byte swizzle): a slot that has been read is refilled at once, into the
-// CTA's next item where the item's tiles are all on the way, and no warp waits
-// for another inside an item.  16 rows are half of the smallest tcgen05 tile's
-// quarter, and S and P would go through tensor memory between two products of a
-// few hundred cycles; mma.sync (m16n8k16) keeps them in registers and needs a
-// tenth of the time the tile's bytes take to arrive.  Two CTAs per SM, each with
-// 96 KB of tiles in flight or in use, so that one CTA's item ends are covered by
-// the other's loads.  Measured: one token of each of 64 sequences of 16,000 (4.3
-// GB of K and V) 665 us, 6.5 TB/s, with pages of 8 tokens 6.2; one token over 300
-// 7.5 us, a chain of latencies.  One loading warp for all four, with larger boxes
-// and a barrier per tile, took 650 us for the former (5.9 TB/s with pages of 8)
-// and 9.8 for the latter.
+// A tile is 64 keys.  One warp fetches tiles with TMA (a lane to K and one to V
+// of each page, both halves of head_dim in one box, 128-byte swizzle), into the
+// CTA's next items while the last ones are worked on; four warps each take 16 of
+// a tile's keys with statistics and O of their own, joined when the item ends:
+// no barrier between the four inside an item.  16 rows are half of the smallest
+// tcgen05 tile's quarter, and S and P would go through tensor memory between two
+// products of a few hundred cycles; mma.sync (m16n8k16) keeps them in registers
+// and needs a tenth of the time the tile's bytes take to arrive.  Two CTAs per
+// SM, each with 96 KB of tiles in flight or in use, so that one CTA's item ends
+// are covered by the other's loads.
+// Measured: one token of each of 64 sequences of 16,000 (4.3 GB of K and V)
+// 640 us, 6.6 TB/s, with pages of 8 tokens 6.4; one token over 300 6.6 us, a
+// chain of latencies.  A ring of its own for each of the four warps, which it
+// fills itself, took 665 and 7.5.
 #include "kernels.cuh"
 #include "pages.cuh"
 
@@ -30,20 +29,21 @@ namespace duolm {
 namespace {
 
 constexpr int kTile = 64, kRows = 16;
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kOwn = kTile / kWarps;  // a warp's keys of a tile
+constexpr int kWarps = 4, kMath = 32 * kWarps, kThreads = kMath + 32, kOwn = kTile / kWarps;  // a warp's keys of a tile
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int HD>
 struct Lay {
   static constexpr int NH = HD / 64;                   // 64-element halves of a row
-  static constexpr int HALF = kOwn * 128;              // one half of a warp's keys
-  static constexpr int STAGE = 2 * NH * HALF;          // K, then V
-  static constexpr int STAGES = 24 * 1024 / STAGE;     // of a warp: 3 (head_dim 128) or 6
+  static constexpr int STAGE = 2 * NH * kTile * 128;   // K, then V
+  static constexpr int STAGES = 96 * 1024 / STAGE;     // 3 (head_dim 128) or 6
   static constexpr int LD = HD + 8;                    // row of the joined O: 8 banks on per row
-  static constexpr int ACC = kWarps * STAGES * STAGE;  // float [warp][4][LD]
+  static constexpr int ACC = STAGES * STAGE;           // float [warp][4][LD]
   static constexpr int STAT = ACC + kWarps * 4 * LD * 4, BAR = STAT + kWarps * kRows * 8;
-  static constexpr int SMEM = BAR + 8 * kWarps * STAGES + 16 + 1024;
+  static constexpr int SMEM = BAR + 16 * STAGES + 16 + 1024;
 };
+
+__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -85,94 +85,82 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = smem_u32(smem) + warp * STAGES * L::STAGE, bars = smem_u32(smem) + L::BAR + warp * STAGES * 8;
-  int* s_last = reinterpret_cast<int*>(smem + L::BAR + 8 * kWarps * STAGES);
+  const uint32_t sbase = smem_u32(smem);
+  auto full = [&](uint32_t s) { return sbase + L::BAR + 16 * s; };
+  auto empty = [&](uint32_t s) { return sbase + L::BAR + 16 * s + 8; };
+  int* s_last = reinterpret_cast<int*>(smem + L::BAR + 16 * STAGES);
   float* acc = reinterpret_cast<float*>(smem + L::ACC);
   float2* stat = reinterpret_cast<float2*>(smem + L::STAT);  // [warp][row] m, l
 
   pdl_launch_dependents();
-  if (lane == 0) {
-    if (warp == 0) {
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
+  if (warp == kWarps && lane == 0) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kWarps);
     }
-    for (int s = 0; s < STAGES; ++s) mbar_init(bars + 8 * s, 1);
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait();
   if (!plan_usable(p, pl, blockIdx.x)) return;
   const int cta = blockIdx.x, G = a.group;
-
-  // ---- loads.  The cursor: the next tile to fetch, of the item at hand or
-  // (c_next) of the one behind it, that item's end, table, keys and KV head.
-  // Lane 2 j + v fetches K (v = 0) or V (1) of box j of the warp's keys; c_id is
-  // the page that it lies in.
-  const int box_shift = min(p.page_shift, 4), box = 1 << box_shift, n_box = kOwn >> box_shift, chunk = NH * box * 128;
-  static_assert(kOwn == 16, "box_shift");
   PageItem it;
   ItemWalk walk(pl, cta);
-  bool have = walk.next(&it);
-  uint32_t n = 0, m_issued = 0;  // tiles read, tiles fetched
-  bool c_next = false, c_ok = false;
-  int c_t = walk.t0, c_end = walk.t1, c_keys = it.n_keys, c_head = it.kv_head, c_id = -1;
-  const int32_t* c_table = p.table + (int64_t)it.seq * p.max_pages;
-  auto page_of = [&](int t, int j) {
-    const int key = t * kTile + warp * kOwn + j * box;
-    return key < c_keys ? c_table[key >> p.page_shift] : -1;
-  };
-  auto seek = [&]() {
-    if (c_t >= c_end && !c_next && walk.w.unit < walk.w.end) {
-      const PageItem& x = walk.next_item;
-      c_next = true;
-      c_t = 0;
-      c_end = min(x.n_tiles, (min(x.unit0 + walk.units_of(x), walk.w.end) - x.unit0) << walk.w.grain);
-      c_keys = x.n_keys;
-      c_head = x.kv_head;
-      c_table = p.table + (int64_t)x.seq * p.max_pages;
+  // a page's rows of a tile: both halves of K (V), one behind the other
+  const int box_shift = min(p.page_shift, 6), box = 1 << box_shift, n_box = kTile >> box_shift, chunk = NH * box * 128;
+  static_assert(kTile == 64, "box_shift");
+
+  if (warp == kWarps) {
+    // ---- TMA: lane 2 j + v fetches K (v = 0) or V (1) of box j
+    const CUtensorMap* map = lane & 1 ? &tmV : &tmK;
+    const uint32_t dst = sbase + (lane & 1) * NH * kTile * 128 + (lane >> 1) * chunk;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(&it)) {
+      const int32_t* table = p.table + (int64_t)it.seq * p.max_pages;
+      auto fetch = [&](int t) {
+        const int key = t * kTile + (lane >> 1) * box;
+        return lane < 2 * n_box && key < it.n_keys ? table[key >> p.page_shift] : -1;
+      };
+      int id = fetch(walk.t0);
+      for (int t = walk.t0; t < walk.t1; ++t, ++n) {
+        const uint32_t slot = n % STAGES;
+        const int next_id = t + 1 < walk.t1 ? fetch(t + 1) : -1;
+        const int left = it.n_keys - t * kTile;
+        const int boxes = left <= 0 ? 0 : min(n_box, (left + box - 1) >> box_shift);
+        const bool have = lane < 2 * boxes;
+        if (have && (unsigned)id >= (unsigned)p.n_pages) {
+          raise_on_plan(p, pl, ERR_BAD_INDEX, 120);
+          id = 0;
+        }
+        const int y = ((id * p.n_kv_heads + it.kv_head) << p.page_shift) + ((t * kTile + (lane >> 1) * box) & (p.page_tokens - 1));
+        if (!(ok = mbar_wait_warp(empty(slot), (n / STAGES & 1u) ^ 1u, p.st, 121))) break;
+        if (lane == 0) mbar_arrive_expect_tx(full(slot), 2 * boxes * chunk);
+        __syncwarp();
+        if (have) tma_load_3d(map, dst + slot * L::STAGE, full(slot), 0, y, 0);
+        id = next_id;
+      }
     }
-    c_ok = c_t < c_end;
-    if (c_ok && lane < 2 * n_box) c_id = page_of(c_t, lane >> 1);
-  };
-  const CUtensorMap* map = lane & 1 ? &tmV : &tmK;
-  const uint32_t lane_dst = ring + (lane & 1) * NH * L::HALF + (lane >> 1) * chunk;
-  auto issue = [&](int id) {
-    const uint32_t slot = m_issued % STAGES, b = bars + 8 * slot;
-    const int k0 = c_t * kTile + warp * kOwn, left = c_keys - k0;  // the warp's keys
-    const int boxes = left <= 0 ? 0 : min(n_box, (left + box - 1) >> box_shift);
-    const bool mine = lane < 2 * boxes;
-    if (mine && (unsigned)id >= (unsigned)p.n_pages) {
-      raise_on_plan(p, pl, ERR_BAD_INDEX, 120);
-      id = 0;
-    }
-    if (lane == 0) mbar_arrive_expect_tx(b, 2 * boxes * chunk);
-    __syncwarp();
-    if (mine)
-      tma_load_3d(map, lane_dst + slot * L::STAGE, b, 0,
-                  ((id * p.n_kv_heads + c_head) << p.page_shift) + ((k0 + (lane >> 1) * box) & (p.page_tokens - 1)), 0);
-    ++m_issued;
-    ++c_t;
-  };
-  if (have) {
-    // the first tiles' pages in one look
-    const int per = 2 * n_box, s = lane >> (5 - box_shift);  // (per = 2^(5 - box_shift))
-    const int first = s < STAGES && c_t + s < c_end ? page_of(c_t + s, (lane & (per - 1)) >> 1) : -1;
-    for (int k = 0; k < STAGES && c_t < c_end; ++k) issue(__shfl_sync(0xffffffffu, first, k * per + (lane & (per - 1))));
-    seek();
+    // leave no copy in flight into shared memory that this CTA gives up
+    if (!ok)
+      for (uint32_t k = n > STAGES ? n - STAGES : 0; k < n; ++k) mbar_wait_warp(full(k % STAGES), k / STAGES & 1u, p.st, 122);
+    return;
   }
 
   // ---- keys [16 warp, 16 warp + 16) of every tile
   const int g = lane >> 2, c2 = (lane & 3) * 2;
   const float scale_log2 = a.scale * 1.4426950408889634f;
   // lane's row of the four 8 x 8 matrices that one ldmatrix reads
-  const int k_key = (lane >> 4) * 8 + (lane & 7), k_chunk = lane >> 3 & 1;
-  const int v_key = (lane >> 3 & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
+  const int k_key = warp * kOwn + (lane >> 4) * 8 + (lane & 7), k_chunk = lane >> 3 & 1;
+  const int v_key = warp * kOwn + (lane >> 3 & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
   const uint32_t half = box * 128;  // a box's second half lies behind its first
   const uint32_t k_off = (k_key >> box_shift) * chunk + (k_key & (box - 1)) * 128,
                  v_off = (v_key >> box_shift) * chunk + (v_key & (box - 1)) * 128;
+  uint32_t n = 0;
   bool ok = true;
-  uint32_t lost = 0;  // where a wait gave up
-  while (have) {
+  while (walk.next(&it)) {
     const int rows = min(kRows, it.n_rows * G);
     // Q as the products' first operand: rows g and g + 8, elements 16 k + c2.. and 16 k + 8 + c2..
     uint32_t qf[HD / 16][4];
@@ -194,11 +182,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     for (int t = walk.t0; t < walk.t1; ++t, ++n) {
       const uint32_t slot = n % STAGES;
-      if (ok && !(ok = mbar_wait_warp(bars + 8 * slot, n / STAGES & 1u, p.st, 123))) lost = n;
+      ok = ok && mbar_wait_warp(full(slot), n / STAGES & 1u, p.st, 123);
       if (!ok) continue;
       const int k0 = t * kTile + warp * kOwn;
       if (k0 < it.n_keys) {
-        const uint32_t kb = ring + slot * L::STAGE + k_off, vb = ring + slot * L::STAGE + NH * L::HALF + v_off;
+        const uint32_t kb = sbase + slot * L::STAGE + k_off, vb = sbase + slot * L::STAGE + NH * kTile * 128 + v_off;
         float s[4][4] = {};  // two chains per 8 keys, so that the products do not wait on one another
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
@@ -254,11 +242,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           mma16<BF16>(o[2 * c + 1], pf, vf[2] & lo, vf[3] & hi);
         }
       }
-      __syncwarp();  // every lane has read the slot
-      while (c_ok && m_issued - n <= STAGES) {
-        issue(c_id);
-        seek();
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(slot));
     }
     // ---- the item's end: the four warps' parts joined, four rows at a time, an
     // element (four columns of a row) to a thread, in warp order
@@ -288,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int t = 0; t < NT; ++t)
           *reinterpret_cast<float2*>(acc + (warp * 4 + (g & 3)) * L::LD + t * 8 + c2) =
               make_float2(o[t][2 * (q >> 1)], o[t][2 * (q >> 1) + 1]);
-      __syncthreads();
+      math_sync();
       const int r = 4 * q + threadIdx.x / W4, c = threadIdx.x % W4;
       if (threadIdx.x < 4 * W4 && r < rows) {
         float mm = -INFINITY, ll = 0.f;
@@ -314,22 +299,22 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (c == 0) __stcg(reinterpret_cast<float2*>(part + kRows * HD) + r, make_float2(mm, ll));
         }
       }
-      __syncthreads();  // acc and stat are read
+      math_sync();  // acc and stat are read
     }
     if (!whole) {
       // divided among CTAs: the last to arrive joins the parts, in CTA order
       __threadfence();
-      __syncthreads();
+      math_sync();
       const int c0 = walk.first_cta(it), c1 = walk.last_cta(it);
       if (threadIdx.x == 0) {
         const int k = atomicAdd(&pl.arrived[walk.index], 1);
         *s_last = k == c1 - c0;
         if (*s_last) pl.arrived[walk.index] = 0;
       }
-      __syncthreads();
+      math_sync();
       if (*s_last && ok) {
         __threadfence();
-        for (int e = threadIdx.x; e < rows * W4; e += kThreads) {
+        for (int e = threadIdx.x; e < rows * W4; e += kMath) {
           const int r = e / W4;
           auto stat_of = [&](int c) { return __ldcg(reinterpret_cast<const float2*>(part_of(pl, kPart, c, c == c0) + kRows * HD) + r); };
           float mm = -INFINITY, ll = 0.f;
@@ -353,21 +338,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // (the flag is next written behind two of the next item's barriers)
     }
-    have = walk.next(&it);
-    if (have && ok) {
-      c_next = false;  // the cursor has been in this item since its last tile was on the way
-      seek();
-      while (c_ok && m_issued - n < STAGES) {
-        issue(c_id);
-        seek();
-      }
-    }
   }
-  if (!ok) {
-    if (lane == 0) pl.head->stale = 1;
-    // leave no copy in flight into shared memory that this CTA gives up
-    for (uint32_t k = lost + 1; k < m_issued; ++k) mbar_wait_warp(bars + 8 * (k % STAGES), k / STAGES & 1u, p.st, 122);
-  }
+  if (!ok && lane == 0) pl.head->stale = 1;
 }
 
 namespace {
@@ -389,7 +361,7 @@ cudaError_t pages_attention_few(const PagesView& p, const PagesPlan& pl, const A
   CUtensorMap tk, tv;
   char err[128];
   const uint64_t rows = (uint64_t)p.n_pages * p.n_kv_heads * p.page_tokens;
-  const uint32_t box = std::min(p.page_tokens, kOwn);
+  const uint32_t box = std::min(p.page_tokens, kTile);
   const int64_t off = a.layer * p.layer_bytes();
   // {64 elements, cache rows, halves of head_dim}
   const uint64_t dims[3] = {64, rows, (uint64_t)p.head_dim / 64}, strides[2] = {(uint64_t)p.head_dim * 2, 128};
