@@ -477,7 +477,8 @@ int duolm_pages_check(const duolm_pages *pages, void *cuda_stream);
  */
 typedef struct {
   int32_t n;              /* entries */
-  int32_t n_rows;         /* rows of the arrays; offset[n] may be less: rows behind it are left alone */
+  int32_t n_rows;         /* rows of the arrays; offset[n] may be less: rows behind it are left alone.
+                             n_rows * n_q_heads < 2^30 */
   int32_t max_rows;       /* no entry has more rows (chooses the kernel; a larger entry is still right) */
   int32_t n_q_heads;      /* a multiple of n_kv_heads, at most 64 times as many */
   int32_t causal;         /* 1: row j sees the tokens up to its own; 0: every row sees the whole sequence */

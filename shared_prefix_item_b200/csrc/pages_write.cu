@@ -436,8 +436,9 @@ int batch_check(const PagesView& p, const duolm_pages_batch* b) {
     return pages_fail(DUOLM_E_ARG, "batch: a size out of range, or query heads not a multiple of KV heads");
   if (b->n_q_heads / p.n_kv_heads > 64) return pages_fail(DUOLM_E_ARG, "batch: more than 64 query heads per KV head");
   if (b->n > p.n_seqs) return pages_fail(DUOLM_E_ARG, "batch: %d entries for %d sequences (one each)", b->n, p.n_seqs);
-  if ((int64_t)b->n_rows * b->n_q_heads > INT32_MAX)
-    return pages_fail(DUOLM_E_CAPACITY, "batch: 2^31 query rows x heads and more");
+  // (half of int32's range: a grid's step past the last row stays within it)
+  if ((int64_t)b->n_rows * b->n_q_heads > INT32_MAX / 2)
+    return pages_fail(DUOLM_E_CAPACITY, "batch: 2^30 query rows x heads and more");
   if (b->n == 0 || b->n_rows == 0) return 0;
   if (!b->seq || !b->offset || !b->plan) return pages_fail(DUOLM_E_ARG, "batch: null array");
   if (reinterpret_cast<uintptr_t>(b->plan) & 127) return pages_fail(DUOLM_E_ARG, "batch: plan not 128-byte aligned");

@@ -89,7 +89,8 @@ def test_nothing_to_do_is_no_error():
 @pytest.mark.parametrize("over, code", [
     (dict(n_rows=-1), -1), (dict(max_rows=-1), -1), (dict(n_q_heads=0), -1), (dict(n_q_heads=3), -1),
     (dict(n_q_heads=130), -1), (dict(seq=None), -1), (dict(offset=None), -1), (dict(plan=None), -1),
-    (dict(plan=A + 64), -1), (dict(n_rows=1 << 30), -5)])
+    (dict(plan=A + 64), -1), (dict(n_rows=1 << 30), -5), (dict(n_rows=1 << 28), -5),
+    (dict(n_rows=(1 << 30) + 1, n_q_heads=2), -5)])
 def test_a_bad_batch_is_refused(over, code):
     p, b = pages(), batch(**over)
     r, rb = ctypes.byref(p), ctypes.byref(b)
